@@ -17,6 +17,10 @@ Low level (same names and arguments as the C ABI, pointers as ints, raising
     sgemm_selftest_wait_timeout, sgemm_status_string, sgemm_algo_name,
     sgemm_version
 High level (torch tensors): ``gemm``, ``gemm_strided_batched``, ``transpose``.
+
+The linear layer in 8-bit floating point (module ``fp8``, ``include/sgemm_fp8.h``):
+``gemm_fp8``, ``quantize_fp8``, ``quantize_fp8_both``, ``rms_norm_fp8``,
+``rms_norm_backward`` on torch tensors, and the ``sgemm_*`` functions they call.
 """
 from ._binding import (  # noqa: F401
     ALGO_AUTO, ALGO_NAIVE, ALGO_REG_2X2, ALGO_REG_4X4, ALGO_SIMT_CPASYNC, ALGO_SIMT_TMA,
@@ -27,3 +31,21 @@ from ._binding import (  # noqa: F401
     sgemm_select_algo, sgemm_selftest_wait_timeout, sgemm_set_wait_budget_ns,
     sgemm_status_string, sgemm_strided_batched, sgemm_transpose, sgemm_version,
     gemm_strided_batched, transpose)
+
+_FP8_NAMES = (
+    "RmsNormFp8", "gemm_fp8", "quantize_fp8", "quantize_fp8_both", "rms_norm_backward", "rms_norm_fp8", "sgemm_fp8",
+    "sgemm_fp8_quantize", "sgemm_fp8_quantize_both", "sgemm_rms_norm_backward", "sgemm_rms_norm_backward_workspace",
+    "sgemm_rms_norm_fp8")
+
+
+def __getattr__(name):
+    """The names of module fp8, which imports torch, on first use."""
+    if name in _FP8_NAMES:
+        from . import fp8
+        globals().update((n, getattr(fp8, n)) for n in _FP8_NAMES)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_FP8_NAMES})
