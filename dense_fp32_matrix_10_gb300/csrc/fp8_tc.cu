@@ -1,0 +1,175 @@
+// fp8_tc.cu -- instances of the tensor-core 8-bit product, the choice between them and
+// their launch.
+#include "fp8_tc.cuh"
+
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "dispatch.h"
+
+namespace sg {
+namespace {
+
+// Tensor map of a stored 8-bit matrix: boxes of 128 bytes x box_rows, 128-byte swizzle, zeros outside.
+bool encode_u8(CUtensorMap *m, const Fp8Operand &x, int64_t rows, int64_t cols, int box_rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  // a single row has no stride to respect
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows == 1 ? (x.ld + 15) / 16 * 16 : x.ld)};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<unsigned char *>(x.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct KernelInfo {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+  int clusters = 0;   // pairs resident at once (GROUP == 2)
+};
+
+template <class Cfg>
+cudaLaunchConfig_t launch_config(unsigned grid, int cluster, cudaStream_t s, cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(Cfg::THREADS);
+  cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cfg;
+}
+
+// Once per device: the kernel's shared memory, its register split, the pairs that fit.
+template <class Cfg>
+const KernelInfo *kernel_info() {
+  static KernelInfo info[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  KernelInfo &i = info[dev];
+  std::call_once(i.once, [&] {
+    i.err = cudaFuncSetAttribute(fp8_tc_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    cudaFuncAttributes a;
+    if (i.err == cudaSuccess) i.err = cudaFuncGetAttributes(&a, fp8_tc_kernel<Cfg>);
+    // setmaxnreg.inc waits until the launch's registers cover the split
+    if (i.err == cudaSuccess && Cfg::SPLIT_REGS && a.numRegs * Cfg::THREADS < Cfg::SPLIT_TOTAL)
+      i.err = cudaErrorInvalidConfiguration;
+    if (i.err == cudaSuccess && Cfg::GROUP == 2) {
+      cudaLaunchAttribute attr[2];
+      const cudaLaunchConfig_t cfg = launch_config<Cfg>(304, 2, nullptr, attr);
+      i.err = cudaOccupancyMaxActiveClusters(&i.clusters, fp8_tc_kernel<Cfg>, &cfg);
+      if (i.err == cudaSuccess && i.clusters < 1) i.err = cudaErrorInvalidConfiguration;
+    }
+    if (i.err != cudaSuccess) cudaGetLastError();
+  });
+  return i.err == cudaSuccess ? &i : nullptr;
+}
+
+// `split`: CTAs per tile (GROUP == 1).
+template <class Cfg>
+cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
+  const KernelInfo *info = kernel_info<Cfg>();
+  if (!info) return cudaErrorInvalidConfiguration;
+  const Fp8Operand &row = Cfg::SWAP ? p.b : p.a, &col = Cfg::SWAP ? p.a : p.b;
+  Fp8TcParams t;
+  t.rows = Cfg::SWAP ? p.N : p.M;
+  t.cols = Cfg::SWAP ? p.M : p.N;
+  CUtensorMap tm_row, tm_col;
+  const auto encode = [&](CUtensorMap *m, const Fp8Operand &x, int outer, int box) {
+    return x.inner_rows ? encode_u8(m, x, p.K, outer, 128) : encode_u8(m, x, outer, p.K, box);
+  };
+  if (!encode(&tm_row, row, t.rows, 128) || !encode(&tm_col, col, t.cols, Cfg::BN / Cfg::GROUP))
+    return cudaErrorInvalidValue;
+  t.row_s = row.s;
+  t.col_s = col.s;
+  t.row_ld = row.lds;
+  t.col_ld = col.lds;
+  t.row_shift = row.shift;
+  t.col_shift = col.shift;
+  t.row_inner = row.inner_rows;
+  t.col_inner = col.inner_rows;
+  t.kblocks = static_cast<int>((static_cast<int64_t>(p.K) + 127) / 128);
+  const int64_t br = 128 * Cfg::GROUP;
+  t.tiles_r = static_cast<int>((t.rows + br - 1) / br);
+  t.tiles_c = static_cast<int>((static_cast<int64_t>(t.cols) + Cfg::BN - 1) / Cfg::BN);
+  const int64_t tiles = static_cast<int64_t>(t.tiles_r) * t.tiles_c;
+  if (tiles * split > 0x7fffffff) return cudaErrorInvalidValue;
+  t.num_tiles = static_cast<int>(tiles);
+  t.group = 8;
+  t.split = split;
+  t.idesc = idesc_fp8(128 * Cfg::GROUP, Cfg::BN, row.e5m2, col.e5m2, row.inner_rows, col.inner_rows);
+  t.C = p.C;
+  t.ldc = p.ldc;
+  t.typeC = p.typeC;
+  t.vecC = aligned_rows(p.C, p.ldc, p.typeC == SGEMM_TYPE_F32 ? 4 : 2, 16);
+  t.alpha = p.alpha;
+  t.beta = p.beta;
+  t.wait_budget_ns = p.wait_budget_ns;
+  t.status = p.status;
+  const int cluster = Cfg::GROUP == 2 ? 2 : split;
+  const int64_t grid = Cfg::GROUP == 2 ? 2 * (tiles < info->clusters ? tiles : info->clusters) : tiles * split;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = launch_config<Cfg>(static_cast<unsigned>(grid), cluster, s, attr);
+  return cudaLaunchKernelEx(&cfg, fp8_tc_kernel<Cfg>, tm_row, tm_col, t);
+}
+
+using Pair = Fp8Tc<2, 256, false, false, 6, 1>;      // 256 x 256 on two SMs
+using PairVec = Fp8Tc<2, 256, false, true, 6, 1>;
+using Tile = Fp8Tc<1, 128, false, false, 3, 2>;      // 128 x 128, two CTAs an SM
+using TileVec = Fp8Tc<1, 128, false, true, 3, 2>;
+using Narrow = Fp8Tc<1, 64, false, true, 4, 2>;      // up to 64 columns of C
+using Few16 = Fp8Tc<1, 16, true, true, 6, 2>;        // up to 16, 32, 64 rows of C (its columns are the
+using Few32 = Fp8Tc<1, 32, true, true, 5, 2>;        // tile's rows)
+using Few64 = Fp8Tc<1, 64, true, true, 4, 2>;
+
+bool tma_readable(const Fp8Operand &x, int64_t stored_rows) {
+  return reinterpret_cast<uintptr_t>(x.q) % 16 == 0 && (x.ld % 16 == 0 || stored_rows == 1);
+}
+
+// CTAs per tile: as many as keep every CTA resident and give each at least two blocks.
+int pick_split(int64_t tiles, int64_t kblocks, int64_t slots) {
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= slots && kblocks >= 4 * split) split *= 2;
+  return split;
+}
+
+}  // namespace
+
+bool fp8_tc_eligible(const Fp8Params &p) {
+  return tma_readable(p.a, p.a.inner_rows ? p.K : p.M) && tma_readable(p.b, p.b.inner_rows ? p.K : p.N);
+}
+
+cudaError_t launch_fp8_tc(const Fp8Params &p, int sm_count, cudaStream_t s) {
+  const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  const int64_t kb = cdiv(p.K, 128), slots = 2 * sm_count;
+  if (p.M <= 64 && !p.a.inner_rows) {
+    const int split = pick_split(cdiv(p.N, 128), kb, slots);
+    if (p.M <= 16) return launch<Few16>(p, split, s);
+    return p.M <= 32 ? launch<Few32>(p, split, s) : launch<Few64>(p, split, s);
+  }
+  if (p.N <= 64 && !p.b.inner_rows) return launch<Narrow>(p, pick_split(cdiv(p.M, 128), kb, slots), s);
+  const int64_t pairs = cdiv(p.M, 256) * cdiv(p.N, 256), tiles = cdiv(p.M, 128) * cdiv(p.N, 128);
+  const bool vec = p.b.shift == 0;
+  if (pairs * 2 >= sm_count) return vec ? launch<PairVec>(p, 1, s) : launch<Pair>(p, 1, s);
+  const int split = pick_split(tiles, kb, slots);
+  return vec ? launch<TileVec>(p, split, s) : launch<Tile>(p, split, s);
+}
+
+}  // namespace sg

@@ -1,0 +1,555 @@
+// fp8_tc.cuh -- the block-scaled 8-bit product on the 5th-generation tensor
+// cores (tcgen05, kind::f8f6f4, FP32 accumulators in tensor memory).
+//
+//   C[m,n] = alpha * sum_b SA(m,b) SB(n,b) * (sum_{k in block b} A(m,k) B(k,n)) + beta * C[m,n]
+//
+// A stage holds one block of 128 k of both operands: 128 bytes, one row of the
+// 128-byte swizzle, in either orientation (k-contiguous rows, or outer-contiguous
+// rows of a k-major slice: the MMA reads both).  Four MMAs of k = 32 sum a block
+// into a fresh accumulator in tensor memory; the epilogue warps scale it and add
+// it to FP32 registers while the next blocks are multiplied, so the tensor cores'
+// truncating accumulator never holds more than 128 products and every scale is
+// applied in FP32.
+//
+// The tile's rows (tensor memory lanes, one per thread) come from the operand
+// `row`, its columns from `col`.  A row's scale is one value per thread and block;
+// a column's scale is one value for 128 columns, or one each (VEC).
+//
+// Roles (per CTA):
+//   warp 0   TMA producer (one thread)
+//   warp 1   tensor memory; in the (even) CTA one thread issues the MMAs
+//   warp 2   copies the block's scales into a ring in shared memory (cp.async: any
+//            stride, zeros past the edge)
+//   warp 3   idle
+//   warps 4+ epilogue; warp 4 + q + 4 h owns rows 32 q .. +31 and the h-th ECOLS columns
+// Every wait on an mbarrier is bounded; after giving up, a role lets its copies and
+// MMAs land (bounded) and goes to the barriers at the end.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "fp8.cuh"
+#include "fp8.h"
+#include "ptx.cuh"
+#include "simt_gemm.cuh"   // tile_coords
+
+namespace sg {
+
+struct Fp8TcParams {
+  const float *row_s, *col_s;         // scales
+  int64_t row_ld, col_ld;             // their row strides
+  int row_shift, col_shift;           // outer index >> shift = scale index
+  int row_inner, col_inner;           // the scales (and the operand) have k along their rows
+  int rows, cols, kblocks;            // extents of the two outer dimensions, blocks of k
+  int tiles_r, tiles_c, num_tiles, group;
+  int split;                          // CTAs of a cluster that share a tile's blocks (GROUP == 1)
+  uint32_t idesc;
+  void *C;
+  int64_t ldc;
+  int typeC, vecC;
+  float alpha, beta;
+  uint64_t wait_budget_ns;
+  int *status;
+};
+
+// GROUP 2: a pair of CTAs computes 256 x BN (cta_group::2), each holding 128 rows and
+// half of the columns' operand.  SWAP: the tile's columns are C's rows.
+template <int GROUP_, int BN_, bool SWAP_, bool VEC_, int STAGES_, int CTAS_>
+struct Fp8Tc {
+  static constexpr int GROUP = GROUP_, BN = BN_, STAGES = STAGES_, CTAS = CTAS_;
+  static constexpr bool SWAP = SWAP_, VEC = VEC_;
+  static constexpr int ROW_BYTES = 128 * 128, COL_BYTES = BN / GROUP * 128;
+  static constexpr int STAGE_BYTES = ROW_BYTES + COL_BYTES;
+  static constexpr int ACCS = BN >= 128 ? 2 : BN == 64 ? 4 : 8;   // accumulators
+  static constexpr int TMEM_COLS = ACCS * BN;
+  static constexpr int ECOLS = BN == 256 ? 128 : BN;   // columns a thread adds up
+  static constexpr int EPI_WARPS = 4 * (BN / ECOLS);
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+  static constexpr int CHUNK = ECOLS >= 32 ? 32 : 16;   // columns of one tensor memory load
+  static constexpr int COL_SCALES = VEC ? BN : BN / 128;
+  static constexpr int SCALE_SLOTS = 4, SCALES = 128 + COL_SCALES;
+  static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
+  static constexpr int BAR_OFFSET = SCALE_OFFSET + (SCALE_SLOTS * SCALES * 4 + 15) / 16 * 16;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 2 * SCALE_SLOTS + 1;
+  static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;
+  static_assert(VEC || BN % 128 == 0, "one scale per 128 columns needs whole blocks");
+  static_assert(SMEM_BYTES * CTAS + CTAS * 1024 <= 233472, "shared memory over the SM's limit");
+  static_assert(TMEM_COLS * CTAS <= 512, "tensor memory over the SM's limit");
+  // ECOLS = 128: 128 sums and two chunks of 32 in flight per epilogue thread
+  static constexpr bool SPLIT_REGS = ECOLS == 128;
+  static constexpr int REGS_WG0 = 40, REGS_EPI = BN == 256 ? 232 : 216;
+  static constexpr int SPLIT_TOTAL = 128 * REGS_WG0 + 32 * EPI_WARPS * REGS_EPI;
+  static_assert(!SPLIT_REGS || SPLIT_TOTAL <= THREADS * ((65536 / CTAS / THREADS) & ~7),
+                "register split exceeds the launch budget");
+  // a cluster's partial tiles, [column][row], in the stage ring
+  static constexpr int PART_PITCH = 129;
+  static_assert(GROUP == 2 || BN * PART_PITCH * 4 <= STAGES * STAGE_BYTES, "partial tile does not fit");
+};
+
+template <class Cfg>
+struct Fp8Bars {
+  uint32_t base;
+  __device__ uint32_t full(uint32_t s) const { return base + 8 * s; }
+  __device__ uint32_t empty(uint32_t s) const { return base + 8 * (Cfg::STAGES + s); }
+  __device__ uint32_t acc_full(uint32_t b) const { return base + 8 * (2 * Cfg::STAGES + b); }
+  __device__ uint32_t acc_empty(uint32_t b) const { return base + 8 * (2 * Cfg::STAGES + Cfg::ACCS + b); }
+  __device__ uint32_t sc_full(uint32_t r) const { return base + 8 * (2 * Cfg::STAGES + 2 * Cfg::ACCS + r); }
+  __device__ uint32_t sc_empty(uint32_t r) const {
+    return base + 8 * (2 * Cfg::STAGES + 2 * Cfg::ACCS + Cfg::SCALE_SLOTS + r);
+  }
+  __device__ uint32_t drain() const { return base + 8 * (Cfg::NUM_BARS - 1); }
+};
+
+// D[tmem] (+)= A * B, kind::f8f6f4; one thread.
+template <int GROUP>
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (GROUP == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Shared-memory descriptor of a tile of 128-byte rows with the 128-byte swizzle, groups
+// of 8 rows 1024 bytes apart.  k-contiguous: a row is one outer index, and 32 bytes
+// further along it starts the next MMA's k.  Outer-contiguous: a row is one k of 128
+// outer indices, and the next 32 k are 4096 bytes on; one swizzle atom spans all 128
+// outer indices, so only the stride between groups of 8 k matters (given in both fields).
+__device__ __forceinline__ uint64_t desc_fp8(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1024 >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+
+// Instruction descriptor: F32 accumulator, element types (0 E4M3, 1 E5M2), outer-contiguous
+// operands (bits 15, 16), N and M.
+inline uint32_t idesc_fp8(int M, int N, bool a_e5m2, bool b_e5m2, bool a_mn, bool b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(a_e5m2) << 7) | (static_cast<uint32_t>(b_e5m2) << 10) |
+         (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Wait for this thread's tensor memory loads; the values pass through, so that no use of
+// them can be moved before the wait.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+
+// A CTA's work: tiles t = first, first + step, ... and the blocks [kb0, kb1) of each.
+template <class Cfg>
+struct Fp8Work {
+  int first, step, kb0, kb1;
+  __device__ explicit Fp8Work(const Fp8TcParams &p) {
+    if constexpr (Cfg::GROUP == 2) {
+      first = cluster_id_x();
+      step = cluster_count_x();
+      kb0 = 0;
+      kb1 = p.kblocks;
+    } else {   // one tile per cluster, its blocks shared out over the cluster's CTAs
+      first = blockIdx.x / p.split;
+      step = p.num_tiles;
+      const int r = blockIdx.x % p.split;   // the CTA's rank: clusters are p.split CTAs along x
+      kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * r / p.split);
+      kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (r + 1) / p.split);
+    }
+  }
+};
+
+// First row of this CTA's 128 rows and first column of the tile.
+template <class Cfg>
+__device__ __forceinline__ void fp8_tile(const Fp8TcParams &p, int t, uint32_t rank, int &r0, int &c0) {
+  int tr, tc;
+  tile_coords(t, p.tiles_r, p.tiles_c, p.group, tr, tc);
+  r0 = tr * 128 * Cfg::GROUP + (Cfg::GROUP == 2 ? 128 * static_cast<int>(rank) : 0);
+  c0 = tc * Cfg::BN;
+}
+
+// ------------------------------------------------------------------ producer
+template <class Cfg>
+__device__ __forceinline__ void fp8_produce(const Fp8TcParams &p, const CUtensorMap *tm_row,
+                                            const CUtensorMap *tm_col, uint32_t sbase, const Fp8Bars<Cfg> &bar,
+                                            uint32_t rank) {
+  const Fp8Work<Cfg> w(p);
+  uint32_t it = 0;
+  bool ok = true;
+  for (int t = w.first; t < p.num_tiles && ok; t += w.step) {
+    int r0, c0;
+    fp8_tile<Cfg>(p, t, rank, r0, c0);
+    if (Cfg::GROUP == 2) c0 += Cfg::BN / 2 * static_cast<int>(rank);
+    for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+      const uint32_t s = it % Cfg::STAGES, round = it / Cfg::STAGES;
+      if (round > 0 && !wait_parity_bounded(bar.empty(s), (round - 1) & 1, p.wait_budget_ns, p.status)) {
+        ok = false;
+        break;
+      }
+      const uint32_t st = sbase + s * Cfg::STAGE_BYTES;
+      const int k0 = kb * 128;
+      const int rx = p.row_inner ? r0 : k0, ry = p.row_inner ? k0 : r0;
+      const int cx = p.col_inner ? c0 : k0, cy = p.col_inner ? k0 : c0;
+      if constexpr (Cfg::GROUP == 2) {
+        // both CTAs' copies are counted on the even CTA's barrier
+        if (rank == 0) mbar_arrive_expect_tx(bar.full(s), 2 * Cfg::STAGE_BYTES);
+        const uint32_t full = map_to_rank(bar.full(s), 0);
+        tma_load_2d_pair(st, tm_row, full, rx, ry);
+        tma_load_2d_pair(st + Cfg::ROW_BYTES, tm_col, full, cx, cy);
+      } else {
+        mbar_arrive_expect_tx(bar.full(s), Cfg::STAGE_BYTES);
+        tma_load_2d(st, tm_row, bar.full(s), rx, ry);
+        tma_load_2d(st + Cfg::ROW_BYTES, tm_col, bar.full(s), cx, cy);
+      }
+    }
+  }
+  if (!ok && rank == 0) {   // the copies in flight land before the CTA may end
+    for (uint32_t j = it > Cfg::STAGES ? it - Cfg::STAGES : 0; j < it; ++j)
+      wait_parity_bounded(bar.full(j % Cfg::STAGES), (j / Cfg::STAGES) & 1, p.wait_budget_ns, nullptr);
+  }
+}
+
+// ------------------------------------------------------------------ MMA issue
+template <class Cfg>
+__device__ __forceinline__ void fp8_issue(const Fp8TcParams &p, uint32_t sbase, uint32_t tmem,
+                                          const Fp8Bars<Cfg> &bar) {
+  const Fp8Work<Cfg> w(p);
+  const uint32_t row_step = p.row_inner ? 4096 : 32, col_step = p.col_inner ? 4096 : 32;
+  uint32_t it = 0;
+  bool ok = true;
+  for (int t = w.first; t < p.num_tiles && ok; t += w.step) {
+    for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+      const uint32_t b = it % Cfg::ACCS, use = it / Cfg::ACCS;
+      const uint32_t s = it % Cfg::STAGES, round = it / Cfg::STAGES;
+      ok = (use == 0 || wait_parity_bounded(bar.acc_empty(b), (use - 1) & 1, p.wait_budget_ns, p.status)) &&
+           wait_parity_bounded(bar.full(s), round & 1, p.wait_budget_ns, p.status);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t st = sbase + s * Cfg::STAGE_BYTES, d = tmem + b * Cfg::BN;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_fp8<Cfg::GROUP>(d, desc_fp8(st + kk * row_step), desc_fp8(st + Cfg::ROW_BYTES + kk * col_step), p.idesc,
+                            kk > 0);
+      if constexpr (Cfg::GROUP == 2) {
+        mma_commit_pair(bar.empty(s), 0x3);
+        mma_commit_pair(bar.acc_full(b), 0x3);
+      } else {
+        mma_commit(bar.empty(s));
+        mma_commit(bar.acc_full(b));
+      }
+    }
+  }
+  // every MMA issued is complete before tensor memory is released
+  if constexpr (Cfg::GROUP == 2)
+    mma_commit_pair(bar.drain(), 0x1);
+  else
+    mma_commit(bar.drain());
+  wait_parity_bounded(bar.drain(), 0, p.wait_budget_ns, nullptr);
+}
+
+// ------------------------------------------------------------------ scales
+// One warp: block kb's 128 row scales and COL_SCALES column scales into slot it % SLOTS.
+template <class Cfg>
+__device__ __forceinline__ void fp8_scales(const Fp8TcParams &p, uint32_t sbase, const Fp8Bars<Cfg> &bar,
+                                           uint32_t rank, int lane) {
+  const Fp8Work<Cfg> w(p);
+  uint32_t it = 0;
+  for (int t = w.first; t < p.num_tiles; t += w.step) {
+    int r0, c0;
+    fp8_tile<Cfg>(p, t, rank, r0, c0);
+    for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+      const uint32_t slot = it % Cfg::SCALE_SLOTS, round = it / Cfg::SCALE_SLOTS;
+      if (round > 0 && !wait_parity_bounded(bar.sc_empty(slot), (round - 1) & 1, p.wait_budget_ns, p.status)) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+      }
+      const uint32_t dst = sbase + Cfg::SCALE_OFFSET + slot * Cfg::SCALES * 4;
+#pragma unroll
+      for (int i = 0; i < 128; i += 32) {
+        const int r = r0 + i + lane;
+        const bool in = r < p.rows;
+        const int64_t o = in ? r >> p.row_shift : 0;
+        cp_async_4(dst + 4 * (i + lane), p.row_s + (p.row_inner ? kb * p.row_ld + o : o * p.row_ld + kb), in ? 4 : 0);
+      }
+#pragma unroll
+      for (int i = 0; i < Cfg::COL_SCALES; i += 32) {
+        if (i + lane < Cfg::COL_SCALES) {
+          const int c = c0 + (i + lane) * (Cfg::VEC ? 1 : 128);
+          const bool in = c < p.cols;
+          const int64_t o = in ? c >> p.col_shift : 0;
+          cp_async_4(dst + 4 * (128 + i + lane), p.col_s + (p.col_inner ? kb * p.col_ld + o : o * p.col_ld + kb),
+                     in ? 4 : 0);
+        }
+      }
+      cp_async_mbar_arrive_noinc(bar.sc_full(slot));
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ output
+// n <= 8 consecutive elements of a row of C.
+template <class T>
+__device__ __forceinline__ void fp8_put8(const Fp8TcParams &p, T *c, const float (&v)[8], int n) {
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = p.alpha * v[i];
+  if (p.beta != 0.0f) {
+    float old[8];
+    unpack(load8(c, n, p.vecC), old);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] += p.beta * old[i];
+  }
+  store8(c, o, n, p.vecC);
+}
+template <class T>
+__device__ __forceinline__ void fp8_put1(const Fp8TcParams &p, T *c, float v) {
+  v *= p.alpha;
+  if (p.beta != 0.0f) v += p.beta * to_float(*c);
+  from_float(c, v);
+}
+// A thread's ECOLS columns of row r.
+template <class Cfg, class T>
+__device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, const float (&acc)[Cfg::ECOLS]) {
+  if (r >= p.rows) return;
+  T *C = static_cast<T *>(p.C);
+  if constexpr (Cfg::SWAP) {
+#pragma unroll
+    for (int j = 0; j < Cfg::ECOLS; ++j)
+      if (c0 + j < p.cols) fp8_put1(p, C + (c0 + j) * p.ldc + r, acc[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < Cfg::ECOLS; j += 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
+      const int n = p.cols - (c0 + j);
+      if (n > 0) fp8_put8(p, C + r * p.ldc + c0 + j, v, n < 8 ? n : 8);
+    }
+  }
+}
+// This CTA's share of a tile whose partial sums lie in the shared memory of the cluster's
+// CTAs: they are added in the CTAs' order.
+template <class Cfg, class T>
+__device__ __forceinline__ void fp8_reduce(const Fp8TcParams &p, uint32_t sbase, uint32_t rank, int r0, int c0) {
+  const int share = 128 * Cfg::BN / p.split;
+  T *C = static_cast<T *>(p.C);
+  for (int e = threadIdx.x - 128; e < share; e += 32 * Cfg::EPI_WARPS) {
+    // consecutive threads take consecutive elements of a row of C
+    const int row = Cfg::SWAP ? e % 128 : e / Cfg::BN + 128 / p.split * static_cast<int>(rank);
+    const int col = Cfg::SWAP ? e / 128 + Cfg::BN / p.split * static_cast<int>(rank) : e % Cfg::BN;
+    if (r0 + row >= p.rows || c0 + col >= p.cols) continue;
+    const uint32_t at = sbase + 4 * (col * Cfg::PART_PITCH + row);
+    float v = 0.0f;
+    for (int i = 0; i < p.split; ++i) {
+      float x;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_to_rank(at, i)) : "memory");
+      v += x;
+    }
+    const int64_t r = r0 + row, c = c0 + col;
+    fp8_put1(p, C + (Cfg::SWAP ? c * p.ldc + r : r * p.ldc + c), v);
+  }
+}
+
+// ------------------------------------------------------------------ epilogue
+template <class Cfg>
+__device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char *smem, uint32_t sbase, uint32_t tmem,
+                                             const Fp8Bars<Cfg> &bar, uint32_t rank, int q, int half, int lane) {
+  constexpr int EC = Cfg::ECOLS, CH = Cfg::CHUNK;
+  const Fp8Work<Cfg> w(p);
+  const uint32_t lane_addr = (static_cast<uint32_t>(32 * q) << 16) + half * EC;
+  const int row = 32 * q + lane;
+  uint32_t it = 0;
+  for (int t = w.first; t < p.num_tiles; t += w.step) {
+    int r0, c0;
+    fp8_tile<Cfg>(p, t, rank, r0, c0);
+    float acc[EC];
+#pragma unroll
+    for (int j = 0; j < EC; ++j) acc[j] = 0.0f;
+    for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+      const uint32_t b = it % Cfg::ACCS, use = it / Cfg::ACCS;
+      const uint32_t slot = it % Cfg::SCALE_SLOTS, round = it / Cfg::SCALE_SLOTS;
+      const bool ok = wait_parity_bounded(bar.sc_full(slot), round & 1, p.wait_budget_ns, p.status) &&
+                      wait_parity_bounded(bar.acc_full(b), use & 1, p.wait_budget_ns, p.status);
+      if (!__all_sync(~0u, ok)) return;   // the loads below want whole warps
+      const float *sc = reinterpret_cast<const float *>(smem + Cfg::SCALE_OFFSET) + slot * Cfg::SCALES;
+      float rs = sc[row];
+      if (!Cfg::VEC) rs *= sc[128 + (Cfg::BN == 256 ? half : 0)];
+      const float2 rs2 = make_float2(rs, rs);
+      tc_fence_after_sync();
+      const uint32_t src = tmem + lane_addr + b * Cfg::BN;
+      uint32_t v[2][CH];
+      tmem_ld(src, v[0]);
+#pragma unroll
+      for (int cc = 0; cc < EC / CH; ++cc) {
+        uint32_t(&x)[CH] = v[cc & 1];
+        tmem_ld_wait_for(x);
+        if (cc + 1 < EC / CH) {
+          tmem_ld(src + (cc + 1) * CH, v[(cc + 1) & 1]);
+        } else {   // the accumulator has been read: hand it back before the last sums
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (Cfg::GROUP == 2)
+              mbar_arrive_cluster(map_to_rank(bar.acc_empty(b), 0));
+            else
+              mbar_arrive(bar.acc_empty(b));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < CH; j += 4) {
+          float2 a = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+          float2 c = make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+          if constexpr (Cfg::VEC) {
+            const float4 cs = *reinterpret_cast<const float4 *>(sc + 128 + half * EC + cc * CH + j);
+            a = __fmul2_rn(a, make_float2(cs.x, cs.y));
+            c = __fmul2_rn(c, make_float2(cs.z, cs.w));
+          }
+          float *o = acc + cc * CH + j;
+          const float2 s0 = __ffma2_rn(a, rs2, make_float2(o[0], o[1]));
+          const float2 s1 = __ffma2_rn(c, rs2, make_float2(o[2], o[3]));
+          o[0] = s0.x;
+          o[1] = s0.y;
+          o[2] = s1.x;
+          o[3] = s1.y;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.sc_empty(slot));
+    }
+    if (Cfg::GROUP == 1 && p.split > 1) {
+      // every MMA of this CTA has completed, so the stage ring is free
+#pragma unroll
+      for (int j = 0; j < EC; ++j)
+        reinterpret_cast<float *>(smem)[(half * EC + j) * Cfg::PART_PITCH + row] = acc[j];
+    } else {
+      const int c = c0 + half * EC;
+      if (p.typeC == SGEMM_TYPE_F32)
+        fp8_store<Cfg, float>(p, r0 + row, c, acc);
+      else if (p.typeC == SGEMM_TYPE_BF16)
+        fp8_store<Cfg, __nv_bfloat16>(p, r0 + row, c, acc);
+      else
+        fp8_store<Cfg, __half>(p, r0 + row, c, acc);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
+    fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_row, const __grid_constant__ CUtensorMap tm_col,
+                  const __grid_constant__ Fp8TcParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                          ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const Fp8Bars<Cfg> bar{sbase + Cfg::BAR_OFFSET};
+  const uint32_t slot = sbase + Cfg::BAR_OFFSET + Cfg::NUM_BARS * 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool shared_tile = Cfg::GROUP == 1 && p.split > 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(bar.full(s), 1);
+      mbar_init(bar.empty(s), 1);
+    }
+    for (int b = 0; b < Cfg::ACCS; ++b) {
+      mbar_init(bar.acc_full(b), 1);
+      mbar_init(bar.acc_empty(b), Cfg::GROUP * Cfg::EPI_WARPS);
+    }
+    for (int r = 0; r < Cfg::SCALE_SLOTS; ++r) {
+      mbar_init(bar.sc_full(r), 32);
+      mbar_init(bar.sc_empty(r), Cfg::EPI_WARPS);
+    }
+    mbar_init(bar.drain(), 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_row);
+    tma_prefetch_desc(&tm_col);
+  }
+  if (warp == 1) {
+    if constexpr (Cfg::GROUP == 2)
+      tmem_alloc_pair(slot, Cfg::TMEM_COLS);
+    else
+      tmem_alloc(slot, Cfg::TMEM_COLS);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (Cfg::GROUP == 2) cluster_sync();   // the peer's copies and arrivals need initialised barriers
+  tc_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + Cfg::BAR_OFFSET + Cfg::NUM_BARS * 8);
+  griddep_wait();
+  griddep_launch_dependents();   // this CTA has its tensor memory: a dependent cannot take it first
+
+  if (warp < 4) {
+    if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_WG0));
+    if (warp == 0) {
+      if (lane == 0) fp8_produce<Cfg>(p, &tm_row, &tm_col, sbase, bar, Cfg::GROUP == 2 ? rank : 0);
+    } else if (warp == 1) {
+      if (lane == 0 && (Cfg::GROUP == 1 || rank == 0)) fp8_issue<Cfg>(p, sbase, tmem, bar);
+    } else if (warp == 2) {
+      fp8_scales<Cfg>(p, sbase, bar, rank, lane);
+    }
+    __syncwarp();
+    if (shared_tile) cluster_sync();
+  } else {
+    if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_EPI));
+    fp8_epilogue<Cfg>(p, smem, sbase, tmem, bar, rank, warp & 3, (warp >> 2) - 1, lane);
+    __syncwarp();
+    if (shared_tile) {
+      cluster_sync();   // every CTA's partial tile is written
+      int r0, c0;
+      fp8_tile<Cfg>(p, blockIdx.x / p.split, 0, r0, c0);
+      if (p.typeC == SGEMM_TYPE_F32)
+        fp8_reduce<Cfg, float>(p, sbase, rank, r0, c0);
+      else if (p.typeC == SGEMM_TYPE_BF16)
+        fp8_reduce<Cfg, __nv_bfloat16>(p, sbase, rank, r0, c0);
+      else
+        fp8_reduce<Cfg, __half>(p, sbase, rank, r0, c0);
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  // the peers have read this CTA's partial tile; no CTA of a pair releases tensor memory early
+  if (Cfg::GROUP == 2 || shared_tile) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    if constexpr (Cfg::GROUP == 2)
+      tmem_dealloc_pair(tmem, Cfg::TMEM_COLS);
+    else
+      tmem_dealloc(tmem, Cfg::TMEM_COLS);
+  }
+}
+
+}  // namespace sg
