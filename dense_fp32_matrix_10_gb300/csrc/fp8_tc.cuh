@@ -18,8 +18,8 @@
 // Roles (per CTA):
 //   warp 0   TMA producer (one thread)
 //   warp 1   tensor memory; in the (even) CTA one thread issues the MMAs
-//   warp 2   copies the block's scales into a ring in shared memory (cp.async: any
-//            stride, zeros past the edge)
+//   warp 2   VEC: copies a block's column scales into a ring in shared memory (cp.async:
+//            any stride, zeros past the edge)
 //   warp 3   idle
 //   warps 4+ epilogue; warp 4 + q + 4 h owns rows 32 q .. +31 and the h-th ECOLS columns
 // Every wait on an mbarrier is bounded; after giving up, a role lets its copies and
@@ -67,11 +67,11 @@ struct Fp8Tc {
   static constexpr int ECOLS = BN == 256 ? 128 : BN;   // columns a thread adds up
   static constexpr int EPI_WARPS = 4 * (BN / ECOLS);
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-  static constexpr int CHUNK = ECOLS >= 32 ? 32 : 16;   // columns of one tensor memory load
-  static constexpr int COL_SCALES = VEC ? BN : BN / 128;
-  static constexpr int SCALE_SLOTS = 4, SCALES = 128 + COL_SCALES;
+  static constexpr int CHUNK = ECOLS == 128 ? 32 : ECOLS == 64 ? 16 : ECOLS / 2;   // columns of one tensor memory load
+  static_assert(ECOLS / CHUNK % 2 == 0, "chunks alternate between two buffers across blocks");
+  static constexpr int SCALE_SLOTS = VEC ? 4 : 0;   // ring of the columns' scales, a block each
   static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
-  static constexpr int BAR_OFFSET = SCALE_OFFSET + (SCALE_SLOTS * SCALES * 4 + 15) / 16 * 16;
+  static constexpr int BAR_OFFSET = SCALE_OFFSET + SCALE_SLOTS * BN * 4;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 2 * SCALE_SLOTS + 1;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;
   static_assert(VEC || BN % 128 == 0, "one scale per 128 columns needs whole blocks");
@@ -83,9 +83,10 @@ struct Fp8Tc {
   static constexpr int SPLIT_TOTAL = 128 * REGS_WG0 + 32 * EPI_WARPS * REGS_EPI;
   static_assert(!SPLIT_REGS || SPLIT_TOTAL <= THREADS * ((65536 / CTAS / THREADS) & ~7),
                 "register split exceeds the launch budget");
-  // a cluster's partial tiles, [column][row], in the stage ring
-  static constexpr int PART_PITCH = 129;
-  static_assert(GROUP == 2 || BN * PART_PITCH * 4 <= STAGES * STAGE_BYTES, "partial tile does not fit");
+  // a cluster's partial tiles, [row][column], in the stage ring; the pitch is an odd number of 16-byte
+  // units, so that 8 rows of one column group lie in 8 different ones
+  static constexpr int PART_PITCH = BN + 4;
+  static_assert(GROUP == 2 || 128 * PART_PITCH * 4 <= STAGES * STAGE_BYTES, "partial tile does not fit");
 };
 
 template <class Cfg>
@@ -158,6 +159,17 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[16]) {
                :
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
@@ -166,6 +178,13 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
         "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr));
+}
+
+// Arrive on an mbarrier of a CTA of the pair (shared::cluster address).  What the arrival hands over
+// are tensor memory reads that have completed (tcgen05.wait::ld), so it needs no release at cluster
+// scope, which would wait for every memory access of the thread: 185 -> XXX us at 4096^3.
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t cbar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
 
 // A CTA's work: tiles t = first, first + step, ... and the blocks [kb0, kb1) of each.
@@ -250,8 +269,9 @@ __device__ __forceinline__ void fp8_issue(const Fp8TcParams &p, uint32_t sbase, 
     for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
       const uint32_t b = it % Cfg::ACCS, use = it / Cfg::ACCS;
       const uint32_t s = it % Cfg::STAGES, round = it / Cfg::STAGES;
-      ok = (use == 0 || wait_parity_bounded(bar.acc_empty(b), (use - 1) & 1, p.wait_budget_ns, p.status)) &&
-           wait_parity_bounded(bar.full(s), round & 1, p.wait_budget_ns, p.status);
+      // the copies are usually there first: the accumulator's hand-over is the shorter way to the MMA
+      ok = wait_parity_bounded(bar.full(s), round & 1, p.wait_budget_ns, p.status) &&
+           (use == 0 || wait_parity_bounded(bar.acc_empty(b), (use - 1) & 1, p.wait_budget_ns, p.status));
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t st = sbase + s * Cfg::STAGE_BYTES, d = tmem + b * Cfg::BN;
@@ -277,36 +297,35 @@ __device__ __forceinline__ void fp8_issue(const Fp8TcParams &p, uint32_t sbase, 
 }
 
 // ------------------------------------------------------------------ scales
-// One warp: block kb's 128 row scales and COL_SCALES column scales into slot it % SLOTS.
+// Index of the scale of outer index o and block kb.
+__device__ __forceinline__ int64_t scale_index(int o, int kb, int shift, int inner, int64_t ld) {
+  const int64_t i = o >> shift;
+  return inner ? kb * ld + i : i * ld + kb;
+}
+
+// One warp: block kb's BN column scales into slot it % SLOTS.
 template <class Cfg>
 __device__ __forceinline__ void fp8_scales(const Fp8TcParams &p, uint32_t sbase, const Fp8Bars<Cfg> &bar,
                                            uint32_t rank, int lane) {
   const Fp8Work<Cfg> w(p);
   uint32_t it = 0;
-  for (int t = w.first; t < p.num_tiles; t += w.step) {
+  bool ok = true;
+  for (int t = w.first; t < p.num_tiles && ok; t += w.step) {
     int r0, c0;
     fp8_tile<Cfg>(p, t, rank, r0, c0);
     for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
       const uint32_t slot = it % Cfg::SCALE_SLOTS, round = it / Cfg::SCALE_SLOTS;
       if (round > 0 && !wait_parity_bounded(bar.sc_empty(slot), (round - 1) & 1, p.wait_budget_ns, p.status)) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        return;
+        ok = false;
+        break;
       }
-      const uint32_t dst = sbase + Cfg::SCALE_OFFSET + slot * Cfg::SCALES * 4;
+      const uint32_t dst = sbase + Cfg::SCALE_OFFSET + slot * Cfg::BN * 4;
 #pragma unroll
-      for (int i = 0; i < 128; i += 32) {
-        const int r = r0 + i + lane;
-        const bool in = r < p.rows;
-        const int64_t o = in ? r >> p.row_shift : 0;
-        cp_async_4(dst + 4 * (i + lane), p.row_s + (p.row_inner ? kb * p.row_ld + o : o * p.row_ld + kb), in ? 4 : 0);
-      }
-#pragma unroll
-      for (int i = 0; i < Cfg::COL_SCALES; i += 32) {
-        if (i + lane < Cfg::COL_SCALES) {
-          const int c = c0 + (i + lane) * (Cfg::VEC ? 1 : 128);
+      for (int i = 0; i < Cfg::BN; i += 32) {
+        if (i + lane < Cfg::BN) {
+          const int c = c0 + i + lane;
           const bool in = c < p.cols;
-          const int64_t o = in ? c >> p.col_shift : 0;
-          cp_async_4(dst + 4 * (128 + i + lane), p.col_s + (p.col_inner ? kb * p.col_ld + o : o * p.col_ld + kb),
+          cp_async_4(dst + 4 * (i + lane), p.col_s + scale_index(in ? c : 0, kb, p.col_shift, p.col_inner, p.col_ld),
                      in ? 4 : 0);
         }
       }
@@ -357,72 +376,131 @@ __device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, c
     }
   }
 }
-// This CTA's share of a tile whose partial sums lie in the shared memory of the cluster's
-// CTAs: they are added in the CTAs' order.
-template <class Cfg, class T>
+// This CTA's share (rows rank * 128 / SPLIT ..) of a tile whose partial sums lie in the shared memory of
+// the cluster's CTAs: they are added in the CTAs' order, four columns at a time, with sixteen 16-byte
+// reads in flight per thread.
+template <class Cfg, class T, int SPLIT>
 __device__ __forceinline__ void fp8_reduce(const Fp8TcParams &p, uint32_t sbase, uint32_t rank, int r0, int c0) {
-  const int share = 128 * Cfg::BN / p.split;
+  constexpr int ROWS = 128 / SPLIT, UNITS = ROWS * Cfg::BN / 4, THREADS = 32 * Cfg::EPI_WARPS;
+  constexpr int BATCH = SPLIT >= 8 ? 2 : 16 / SPLIT;
   T *C = static_cast<T *>(p.C);
-  for (int e = threadIdx.x - 128; e < share; e += 32 * Cfg::EPI_WARPS) {
-    // consecutive threads take consecutive elements of a row of C
-    const int row = Cfg::SWAP ? e % 128 : e / Cfg::BN + 128 / p.split * static_cast<int>(rank);
-    const int col = Cfg::SWAP ? e / 128 + Cfg::BN / p.split * static_cast<int>(rank) : e % Cfg::BN;
-    if (r0 + row >= p.rows || c0 + col >= p.cols) continue;
-    const uint32_t at = sbase + 4 * (col * Cfg::PART_PITCH + row);
-    float v = 0.0f;
-    for (int i = 0; i < p.split; ++i) {
-      float x;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_to_rank(at, i)) : "memory");
-      v += x;
+  for (int u0 = threadIdx.x - 128; u0 < UNITS; u0 += THREADS * BATCH) {
+    float4 x[BATCH][SPLIT];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      // consecutive threads: consecutive elements of a row of C
+      const int u = min(u0 + k * THREADS, UNITS - 1);
+      const int row = (Cfg::SWAP ? u % ROWS : u / (Cfg::BN / 4)) + ROWS * static_cast<int>(rank);
+      const int col = (Cfg::SWAP ? u / ROWS : u % (Cfg::BN / 4)) * 4;
+      const uint32_t at = sbase + 4 * (row * Cfg::PART_PITCH + col);
+#pragma unroll
+      for (int i = 0; i < SPLIT; ++i) x[k][i] = ld_dsmem_v4(map_to_rank(at, i));
     }
-    const int64_t r = r0 + row, c = c0 + col;
-    fp8_put1(p, C + (Cfg::SWAP ? c * p.ldc + r : r * p.ldc + c), v);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int u = u0 + k * THREADS;
+      if (u >= UNITS) break;
+      const int row = (Cfg::SWAP ? u % ROWS : u / (Cfg::BN / 4)) + ROWS * static_cast<int>(rank);
+      const int col = (Cfg::SWAP ? u / ROWS : u % (Cfg::BN / 4)) * 4;
+      float4 v = x[k][0];
+#pragma unroll
+      for (int i = 1; i < SPLIT; ++i) {
+        v.x += x[k][i].x;
+        v.y += x[k][i].y;
+        v.z += x[k][i].z;
+        v.w += x[k][i].w;
+      }
+      const int64_t r = r0 + row, c = c0 + col;
+      if (r >= p.rows) continue;
+      const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < p.cols) fp8_put1(p, C + (Cfg::SWAP ? (c + j) * p.ldc + r : r * p.ldc + c + j), o[j]);
+    }
   }
+}
+template <class Cfg, class T>
+__device__ __forceinline__ void fp8_reduce_tile(const Fp8TcParams &p, uint32_t sbase, uint32_t rank, int r0, int c0) {
+  if (p.split == 2)
+    fp8_reduce<Cfg, T, 2>(p, sbase, rank, r0, c0);
+  else if (p.split == 4)
+    fp8_reduce<Cfg, T, 4>(p, sbase, rank, r0, c0);
+  else
+    fp8_reduce<Cfg, T, 8>(p, sbase, rank, r0, c0);
 }
 
 // ------------------------------------------------------------------ epilogue
+// The loads of tensor memory run one chunk ahead of the sums, across blocks too: before the last
+// chunk of a block is added, its accumulator has been handed back and the next block's first chunk
+// is on its way.  The row's scales come straight from global memory, a block ahead.
 template <class Cfg>
 __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char *smem, uint32_t sbase, uint32_t tmem,
                                              const Fp8Bars<Cfg> &bar, uint32_t rank, int q, int half, int lane) {
-  constexpr int EC = Cfg::ECOLS, CH = Cfg::CHUNK;
+  constexpr int EC = Cfg::ECOLS, CH = Cfg::CHUNK, NC = EC / CH;
   const Fp8Work<Cfg> w(p);
-  const uint32_t lane_addr = (static_cast<uint32_t>(32 * q) << 16) + half * EC;
+  const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * EC;
   const int row = 32 * q + lane;
   uint32_t it = 0;
+  // accumulator of block `i` is complete (whole warps: the loads want them)
+  const auto acc_ready = [&](uint32_t i) {
+    const bool ok = wait_parity_bounded(bar.acc_full(i % Cfg::ACCS), i / Cfg::ACCS & 1, p.wait_budget_ns, p.status);
+    if (!__all_sync(~0u, ok)) return false;
+    tc_fence_after_sync();
+    return true;
+  };
   for (int t = w.first; t < p.num_tiles; t += w.step) {
     int r0, c0;
     fp8_tile<Cfg>(p, t, rank, r0, c0);
     float acc[EC];
 #pragma unroll
     for (int j = 0; j < EC; ++j) acc[j] = 0.0f;
+    // scales of a row past the edge are those of the last one: its sums are not stored
+    const float *rp = p.row_s + scale_index(min(r0 + row, p.rows - 1), w.kb0, p.row_shift, p.row_inner, p.row_ld);
+    const float *cp = p.col_s + (Cfg::VEC ? 0 : scale_index(min(c0 + half * EC, p.cols - 1), w.kb0, p.col_shift,
+                                                            p.col_inner, p.col_ld));
+    const int64_t rstep = p.row_inner ? p.row_ld : 1, cstep = p.col_inner ? p.col_ld : 1;
+    uint32_t v[2][CH];
+    float rs = 0.0f, cs = 1.0f;
+    if (w.kb0 < w.kb1) {
+      rs = *rp;
+      if (!Cfg::VEC) cs = *cp;
+      if (!acc_ready(it)) return;
+      tmem_ld(src + it % Cfg::ACCS * Cfg::BN, v[0]);
+    }
     for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-      const uint32_t b = it % Cfg::ACCS, use = it / Cfg::ACCS;
-      const uint32_t slot = it % Cfg::SCALE_SLOTS, round = it / Cfg::SCALE_SLOTS;
-      const bool ok = wait_parity_bounded(bar.sc_full(slot), round & 1, p.wait_budget_ns, p.status) &&
-                      wait_parity_bounded(bar.acc_full(b), use & 1, p.wait_budget_ns, p.status);
-      if (!__all_sync(~0u, ok)) return;   // the loads below want whole warps
-      const float *sc = reinterpret_cast<const float *>(smem + Cfg::SCALE_OFFSET) + slot * Cfg::SCALES;
-      float rs = sc[row];
-      if (!Cfg::VEC) rs *= sc[128 + (Cfg::BN == 256 ? half : 0)];
-      const float2 rs2 = make_float2(rs, rs);
-      tc_fence_after_sync();
-      const uint32_t src = tmem + lane_addr + b * Cfg::BN;
-      uint32_t v[2][CH];
-      tmem_ld(src, v[0]);
+      const uint32_t b = it % Cfg::ACCS;
+      const float s = rs * cs;
+      const float2 s2 = make_float2(s, s);
+      const bool more = kb + 1 < w.kb1;
+      if (more) {
+        rs = *(rp += rstep);
+        if (!Cfg::VEC) cs = *(cp += cstep);
+      }
+      const float *sc = nullptr;
+      if constexpr (Cfg::VEC) {
+        const uint32_t slot = it % Cfg::SCALE_SLOTS;
+        const bool ok = wait_parity_bounded(bar.sc_full(slot), it / Cfg::SCALE_SLOTS & 1, p.wait_budget_ns, p.status);
+        if (!__all_sync(~0u, ok)) return;
+        sc = reinterpret_cast<const float *>(smem + Cfg::SCALE_OFFSET) + slot * Cfg::BN + half * EC;
+      }
 #pragma unroll
-      for (int cc = 0; cc < EC / CH; ++cc) {
+      for (int cc = 0; cc < NC; ++cc) {
         uint32_t(&x)[CH] = v[cc & 1];
         tmem_ld_wait_for(x);
-        if (cc + 1 < EC / CH) {
-          tmem_ld(src + (cc + 1) * CH, v[(cc + 1) & 1]);
-        } else {   // the accumulator has been read: hand it back before the last sums
+        if (cc + 1 < NC) {
+          tmem_ld(src + b * Cfg::BN + (cc + 1) * CH, v[(cc + 1) & 1]);
+        } else {
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) {
-            if constexpr (Cfg::GROUP == 2)
-              mbar_arrive_cluster(map_to_rank(bar.acc_empty(b), 0));
+            if (Cfg::GROUP == 2 && rank != 0)
+              mbar_arrive_peer(map_to_rank(bar.acc_empty(b), 0));
             else
               mbar_arrive(bar.acc_empty(b));
+          }
+          if (more) {
+            if (!acc_ready(it + 1)) return;
+            tmem_ld(src + (it + 1) % Cfg::ACCS * Cfg::BN, v[0]);
           }
         }
 #pragma unroll
@@ -430,27 +508,30 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
           float2 a = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
           float2 c = make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
           if constexpr (Cfg::VEC) {
-            const float4 cs = *reinterpret_cast<const float4 *>(sc + 128 + half * EC + cc * CH + j);
-            a = __fmul2_rn(a, make_float2(cs.x, cs.y));
-            c = __fmul2_rn(c, make_float2(cs.z, cs.w));
+            const float4 f = *reinterpret_cast<const float4 *>(sc + cc * CH + j);
+            a = __fmul2_rn(a, make_float2(f.x, f.y));
+            c = __fmul2_rn(c, make_float2(f.z, f.w));
           }
           float *o = acc + cc * CH + j;
-          const float2 s0 = __ffma2_rn(a, rs2, make_float2(o[0], o[1]));
-          const float2 s1 = __ffma2_rn(c, rs2, make_float2(o[2], o[3]));
-          o[0] = s0.x;
-          o[1] = s0.y;
-          o[2] = s1.x;
-          o[3] = s1.y;
+          const float2 o0 = __ffma2_rn(a, s2, make_float2(o[0], o[1]));
+          const float2 o1 = __ffma2_rn(c, s2, make_float2(o[2], o[3]));
+          o[0] = o0.x;
+          o[1] = o0.y;
+          o[2] = o1.x;
+          o[3] = o1.y;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.sc_empty(slot));
+      if constexpr (Cfg::VEC) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.sc_empty(it % Cfg::SCALE_SLOTS));
+      }
     }
     if (Cfg::GROUP == 1 && p.split > 1) {
       // every MMA of this CTA has completed, so the stage ring is free
 #pragma unroll
-      for (int j = 0; j < EC; ++j)
-        reinterpret_cast<float *>(smem)[(half * EC + j) * Cfg::PART_PITCH + row] = acc[j];
+      for (int j = 0; j < EC; j += 4)
+        sts128(sbase + 4 * (row * Cfg::PART_PITCH + half * EC + j),
+               make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
     } else {
       const int c = c0 + half * EC;
       if (p.typeC == SGEMM_TYPE_F32)
@@ -516,7 +597,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
       if (lane == 0) fp8_produce<Cfg>(p, &tm_row, &tm_col, sbase, bar, Cfg::GROUP == 2 ? rank : 0);
     } else if (warp == 1) {
       if (lane == 0 && (Cfg::GROUP == 1 || rank == 0)) fp8_issue<Cfg>(p, sbase, tmem, bar);
-    } else if (warp == 2) {
+    } else if (Cfg::VEC && warp == 2) {
       fp8_scales<Cfg>(p, sbase, bar, rank, lane);
     }
     __syncwarp();
@@ -530,11 +611,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
       int r0, c0;
       fp8_tile<Cfg>(p, blockIdx.x / p.split, 0, r0, c0);
       if (p.typeC == SGEMM_TYPE_F32)
-        fp8_reduce<Cfg, float>(p, sbase, rank, r0, c0);
+        fp8_reduce_tile<Cfg, float>(p, sbase, rank, r0, c0);
       else if (p.typeC == SGEMM_TYPE_BF16)
-        fp8_reduce<Cfg, __nv_bfloat16>(p, sbase, rank, r0, c0);
+        fp8_reduce_tile<Cfg, __nv_bfloat16>(p, sbase, rank, r0, c0);
       else
-        fp8_reduce<Cfg, __half>(p, sbase, rank, r0, c0);
+        fp8_reduce_tile<Cfg, __half>(p, sbase, rank, r0, c0);
       __syncwarp();
     }
   }
