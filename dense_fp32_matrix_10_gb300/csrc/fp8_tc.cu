@@ -105,6 +105,7 @@ cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
   t.col_shift = col.shift;
   t.row_inner = row.inner_rows;
   t.col_inner = col.inner_rows;
+  t.row_vec = !row.inner_rows && aligned_rows(row.s, row.lds, 4, 16);
   t.kblocks = static_cast<int>((static_cast<int64_t>(p.K) + 127) / 128);
   const int64_t br = 128 * Cfg::GROUP;
   t.tiles_r = static_cast<int>((t.rows + br - 1) / br);
@@ -135,7 +136,7 @@ using PairVec = Fp8Tc<2, 256, false, true, 6, 1>;
 using Tile = Fp8Tc<1, 128, false, false, 3, 2>;      // 128 x 128, two CTAs an SM
 using TileVec = Fp8Tc<1, 128, false, true, 3, 2>;
 using Narrow = Fp8Tc<1, 64, false, true, 4, 2>;      // up to 64 columns of C
-using Few16 = Fp8Tc<1, 16, true, true, 6, 2>;        // up to 16, 32, 64 rows of C (its columns are the
+using Few16 = Fp8Tc<1, 16, true, true, 5, 2>;        // up to 16, 32, 64 rows of C (its columns are the
 using Few32 = Fp8Tc<1, 32, true, true, 5, 2>;        // tile's rows)
 using Few64 = Fp8Tc<1, 64, true, true, 4, 2>;
 

@@ -18,8 +18,8 @@
 // Roles (per CTA):
 //   warp 0   TMA producer (one thread)
 //   warp 1   tensor memory; in the (even) CTA one thread issues the MMAs
-//   warp 2   VEC: copies a block's column scales into a ring in shared memory (cp.async:
-//            any stride, zeros past the edge)
+//   warp 2   VEC: copies the scales of four blocks at a time into a ring in shared memory
+//            (cp.async: any stride, zeros past the edge)
 //   warp 3   idle
 //   warps 4+ epilogue; warp 4 + q + 4 h owns rows 32 q .. +31 and the h-th ECOLS columns
 // Every wait on an mbarrier is bounded; after giving up, a role lets its copies and
@@ -42,6 +42,7 @@ struct Fp8TcParams {
   int64_t row_ld, col_ld;             // their row strides
   int row_shift, col_shift;           // outer index >> shift = scale index
   int row_inner, col_inner;           // the scales (and the operand) have k along their rows
+  int row_vec;                        // four consecutive blocks' row scales are an aligned vector
   int rows, cols, kblocks;            // extents of the two outer dimensions, blocks of k
   int tiles_r, tiles_c, num_tiles, group;
   int split;                          // CTAs of a cluster that share a tile's blocks (GROUP == 1)
@@ -67,11 +68,20 @@ struct Fp8Tc {
   static constexpr int ECOLS = BN == 256 ? 128 : BN;   // columns a thread adds up
   static constexpr int EPI_WARPS = 4 * (BN / ECOLS);
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-  static constexpr int CHUNK = ECOLS == 128 ? 32 : ECOLS == 64 ? 16 : ECOLS / 2;   // columns of one tensor memory load
+  // FRAG: a thread holds 4 rows and every fourth pair of columns instead of one row, so it reads a
+  // quarter of the column scales.  A shared memory read fills 128 bytes of registers a cycle however
+  // many lanes share an address: 128 scales for each of 256 threads and block are 1024 cycles, more
+  // than the block's MMAs take (4096 x 4096 x 16384: 448 us with one row a thread, XXX so).
+  static constexpr bool FRAG = VEC && !SWAP && ECOLS == 128;
+  static constexpr int CHUNK = ECOLS == 128 ? 32 : ECOLS == 64 ? 16 : ECOLS / 2;   // columns of a tensor memory load
   static_assert(ECOLS / CHUNK % 2 == 0, "chunks alternate between two buffers across blocks");
-  static constexpr int SCALE_SLOTS = VEC ? 4 : 0;   // ring of the columns' scales, a block each
+  // VEC: ring of scales, SCALE_BLOCKS blocks of k a slot (one wait per slot, not per block): the rows'
+  // [row][block], then the columns' [block][column]
+  static constexpr int SCALE_SLOTS = VEC ? 3 : 0, SCALE_BLOCKS = 4;
+  static constexpr int COL_SCALES = 128 * SCALE_BLOCKS;   // index of the first column scale
+  static constexpr int SCALE_BYTES = 4 * (COL_SCALES + SCALE_BLOCKS * BN);
   static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
-  static constexpr int BAR_OFFSET = SCALE_OFFSET + SCALE_SLOTS * BN * 4;
+  static constexpr int BAR_OFFSET = SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 2 * SCALE_SLOTS + 1;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;
   static_assert(VEC || BN % 128 == 0, "one scale per 128 columns needs whole blocks");
@@ -185,6 +195,28 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
 // scope, which would wait for every memory access of the thread: 185 -> XXX us at 4096^3.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t cbar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
+}
+
+// FRAG: 32 rows x 32 columns in pieces of 8 x 2 per four lanes: lane l gets rows l / 4 + 8 i and
+// columns 8 n + 2 (l % 4) + {0, 1} in v[16 (i / 2) + 4 n + 2 (i % 2) + {0, 1}].
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {   // lanes 0..15, 16..31
+    uint32_t *o = v + 16 * h;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+          "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+        : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16)));
+  }
+}
+template <class Cfg>
+__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&v)[Cfg::CHUNK]) {
+  if constexpr (Cfg::FRAG)
+    tmem_ld_frag(taddr, v);
+  else
+    tmem_ld(taddr, v);
 }
 
 // A CTA's work: tiles t = first, first + step, ... and the blocks [kb0, kb1) of each.
@@ -303,31 +335,50 @@ __device__ __forceinline__ int64_t scale_index(int o, int kb, int shift, int inn
   return inner ? kb * ld + i : i * ld + kb;
 }
 
-// One warp: block kb's BN column scales into slot it % SLOTS.
+// 16-byte asynchronous copy global -> shared; src_bytes = 0 writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
+// One warp: the scales of SCALE_BLOCKS blocks of a tile into slot g % SLOTS.
 template <class Cfg>
 __device__ __forceinline__ void fp8_scales(const Fp8TcParams &p, uint32_t sbase, const Fp8Bars<Cfg> &bar,
                                            uint32_t rank, int lane) {
+  constexpr int SB = Cfg::SCALE_BLOCKS;
   const Fp8Work<Cfg> w(p);
-  uint32_t it = 0;
+  uint32_t g = 0;
   bool ok = true;
   for (int t = w.first; t < p.num_tiles && ok; t += w.step) {
     int r0, c0;
     fp8_tile<Cfg>(p, t, rank, r0, c0);
-    for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-      const uint32_t slot = it % Cfg::SCALE_SLOTS, round = it / Cfg::SCALE_SLOTS;
+    for (int kb0 = w.kb0; kb0 < w.kb1; kb0 += SB, ++g) {
+      const uint32_t slot = g % Cfg::SCALE_SLOTS, round = g / Cfg::SCALE_SLOTS;
       if (round > 0 && !wait_parity_bounded(bar.sc_empty(slot), (round - 1) & 1, p.wait_budget_ns, p.status)) {
         ok = false;
         break;
       }
-      const uint32_t dst = sbase + Cfg::SCALE_OFFSET + slot * Cfg::BN * 4;
-#pragma unroll
-      for (int i = 0; i < Cfg::BN; i += 32) {
-        if (i + lane < Cfg::BN) {
-          const int c = c0 + i + lane;
-          const bool in = c < p.cols;
-          cp_async_4(dst + 4 * (i + lane), p.col_s + scale_index(in ? c : 0, kb, p.col_shift, p.col_inner, p.col_ld),
-                     in ? 4 : 0);
+      const uint32_t dst = sbase + Cfg::SCALE_OFFSET + slot * Cfg::SCALE_BYTES;
+      const int n = min(SB, w.kb1 - kb0);
+      const bool vec = p.row_vec && kb0 % SB == 0 && kb0 + SB <= p.kblocks;
+#pragma unroll 1
+      for (int i = lane; i < 128; i += 32) {
+        const bool in = r0 + i < p.rows;
+        const float *src = p.row_s + scale_index(in ? r0 + i : 0, kb0, p.row_shift, p.row_inner, p.row_ld);
+        if (vec) {
+          cp_async_16(dst + 16 * i, src, in ? 16 : 0);
+        } else {
+          const int64_t step = p.row_inner ? p.row_ld : 1;
+          for (int k = 0; k < n; ++k, src += step) cp_async_4(dst + 16 * i + 4 * k, src, in ? 4 : 0);
         }
+      }
+#pragma unroll 1
+      for (int i = lane; i < Cfg::BN; i += 32) {
+        const int c = c0 + i;
+        const bool in = c < p.cols;
+        const float *src = p.col_s + scale_index(in ? c : 0, kb0, p.col_shift, p.col_inner, p.col_ld);
+        const int64_t step = p.col_inner ? p.col_ld : 1;
+        for (int k = 0; k < n; ++k, src += step)
+          cp_async_4(dst + 4 * (Cfg::COL_SCALES + k * Cfg::BN + i), src, in ? 4 : 0);
       }
       cp_async_mbar_arrive_noinc(bar.sc_full(slot));
     }
@@ -356,12 +407,42 @@ __device__ __forceinline__ void fp8_put1(const Fp8TcParams &p, T *c, float v) {
   if (p.beta != 0.0f) v += p.beta * to_float(*c);
   from_float(c, v);
 }
-// A thread's ECOLS columns of row r.
+// FRAG: row and column, in the warp's 32 x 128, of a thread's sums j and j + 1 (j even; chunks of 32).
+__device__ __forceinline__ int frag_row(int j, int lane) { return lane / 4 + 16 * (j % 32 / 16) + 8 * (j / 2 % 2); }
+__device__ __forceinline__ int frag_col(int j, int lane) { return j / 32 * 32 + j % 16 / 4 * 8 + 2 * (lane & 3); }
+
+// Two consecutive elements of a row of C at an even column, the second if `two`.
+template <class T>
+__device__ __forceinline__ void fp8_put2(const Fp8TcParams &p, T *c, float v0, float v1, bool two) {
+  if (!two || !p.vecC) {
+    fp8_put1(p, c, v0);
+    if (two) fp8_put1(p, c + 1, v1);
+    return;
+  }
+  v0 *= p.alpha;
+  v1 *= p.alpha;
+  if (p.beta != 0.0f) {
+    v0 += p.beta * to_float(c[0]);
+    v1 += p.beta * to_float(c[1]);
+  }
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float2 *>(c) = make_float2(v0, v1);
+  else
+    *reinterpret_cast<uint32_t *>(c) = pack2(v0, v1, T());
+}
+// A thread's sums: ECOLS columns from c0 of row r, or (FRAG) its share of 32 rows from r.
 template <class Cfg, class T>
-__device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, const float (&acc)[Cfg::ECOLS]) {
-  if (r >= p.rows) return;
+__device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, int lane, const float (&acc)[Cfg::ECOLS]) {
   T *C = static_cast<T *>(p.C);
-  if constexpr (Cfg::SWAP) {
+  if constexpr (Cfg::FRAG) {
+#pragma unroll
+    for (int j = 0; j < Cfg::ECOLS; j += 2) {
+      const int row = r + frag_row(j, lane), col = c0 + frag_col(j, lane);
+      if (row < p.rows && col < p.cols) fp8_put2(p, C + row * p.ldc + col, acc[j], acc[j + 1], col + 1 < p.cols);
+    }
+  } else if (r >= p.rows) {
+    return;
+  } else if constexpr (Cfg::SWAP) {
 #pragma unroll
     for (int j = 0; j < Cfg::ECOLS; ++j)
       if (c0 + j < p.cols) fp8_put1(p, C + (c0 + j) * p.ldc + r, acc[j]);
@@ -432,15 +513,15 @@ __device__ __forceinline__ void fp8_reduce_tile(const Fp8TcParams &p, uint32_t s
 // ------------------------------------------------------------------ epilogue
 // The loads of tensor memory run one chunk ahead of the sums, across blocks too: before the last
 // chunk of a block is added, its accumulator has been handed back and the next block's first chunk
-// is on its way.  The row's scales come straight from global memory, a block ahead.
+// is on its way.
 template <class Cfg>
 __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char *smem, uint32_t sbase, uint32_t tmem,
                                              const Fp8Bars<Cfg> &bar, uint32_t rank, int q, int half, int lane) {
-  constexpr int EC = Cfg::ECOLS, CH = Cfg::CHUNK, NC = EC / CH;
+  constexpr int EC = Cfg::ECOLS, CH = Cfg::CHUNK, NC = EC / CH, SB = Cfg::SCALE_BLOCKS;
   const Fp8Work<Cfg> w(p);
   const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * EC;
   const int row = 32 * q + lane;
-  uint32_t it = 0;
+  uint32_t it = 0, group = 0;   // blocks and slots of scales used so far
   // accumulator of block `i` is complete (whole warps: the loads want them)
   const auto acc_ready = [&](uint32_t i) {
     const bool ok = wait_parity_bounded(bar.acc_full(i % Cfg::ACCS), i / Cfg::ACCS & 1, p.wait_budget_ns, p.status);
@@ -454,41 +535,68 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
     float acc[EC];
 #pragma unroll
     for (int j = 0; j < EC; ++j) acc[j] = 0.0f;
-    // scales of a row past the edge are those of the last one: its sums are not stored
-    const float *rp = p.row_s + scale_index(min(r0 + row, p.rows - 1), w.kb0, p.row_shift, p.row_inner, p.row_ld);
-    const float *cp = p.col_s + (Cfg::VEC ? 0 : scale_index(min(c0 + half * EC, p.cols - 1), w.kb0, p.col_shift,
-                                                            p.col_inner, p.col_ld));
-    const int64_t rstep = p.row_inner ? p.row_ld : 1, cstep = p.col_inner ? p.col_ld : 1;
     uint32_t v[2][CH];
-    float rs = 0.0f, cs = 1.0f;
+    // !VEC: one scale per thread and block, loaded a block ahead (in groups of four, 16 bytes at a time,
+    // it was slower: 245 -> 258 us at 4096 x 4096 x 16384).  Those of a row past the edge are the last
+    // one's: its sums are not stored.
+    const float *rp = p.row_s + scale_index(min(r0 + row, p.rows - 1), w.kb0, p.row_shift, p.row_inner, p.row_ld);
+    const float *cp = p.col_s + scale_index(min(c0 + half * EC, p.cols - 1), w.kb0, p.col_shift, p.col_inner, p.col_ld);
+    const int64_t rstep = p.row_inner ? p.row_ld : 1, cstep = p.col_inner ? p.col_ld : 1;
+    float row_s = 0.0f, col_s = 0.0f;
+    if (!Cfg::VEC && w.kb0 < w.kb1) {
+      row_s = *rp;
+      col_s = *cp;
+    }
     if (w.kb0 < w.kb1) {
-      rs = *rp;
-      if (!Cfg::VEC) cs = *cp;
       if (!acc_ready(it)) return;
-      tmem_ld(src + it % Cfg::ACCS * Cfg::BN, v[0]);
+      tmem_ld_chunk<Cfg>(src + it % Cfg::ACCS * Cfg::BN, v[0]);
     }
     for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
       const uint32_t b = it % Cfg::ACCS;
-      const float s = rs * cs;
-      const float2 s2 = make_float2(s, s);
       const bool more = kb + 1 < w.kb1;
-      if (more) {
-        rs = *(rp += rstep);
-        if (!Cfg::VEC) cs = *(cp += cstep);
-      }
-      const float *sc = nullptr;
+      const int i = (kb - w.kb0) % SB;
+      const uint32_t slot = group % (Cfg::VEC ? Cfg::SCALE_SLOTS : 1);
+      const float *sc = reinterpret_cast<const float *>(smem + Cfg::SCALE_OFFSET + slot * Cfg::SCALE_BYTES);
+      float2 rs[4];   // FRAG: the scales of the thread's four rows; else of its one
       if constexpr (Cfg::VEC) {
-        const uint32_t slot = it % Cfg::SCALE_SLOTS;
-        const bool ok = wait_parity_bounded(bar.sc_full(slot), it / Cfg::SCALE_SLOTS & 1, p.wait_budget_ns, p.status);
-        if (!__all_sync(~0u, ok)) return;
-        sc = reinterpret_cast<const float *>(smem + Cfg::SCALE_OFFSET) + slot * Cfg::BN + half * EC;
+        if (i == 0) {
+          const bool ok = wait_parity_bounded(bar.sc_full(slot), group / Cfg::SCALE_SLOTS & 1, p.wait_budget_ns, p.status);
+          if (!__all_sync(~0u, ok)) return;
+        }
+#pragma unroll
+        for (int j = 0; j < (Cfg::FRAG ? 4 : 1); ++j) {
+          const float f = sc[(Cfg::FRAG ? 32 * q + lane / 4 + 8 * j : row) * SB + i];
+          rs[j] = make_float2(f, f);
+        }
+        sc += Cfg::COL_SCALES + i * Cfg::BN + half * EC;
+      } else {
+        const float f = row_s * col_s;
+        rs[0] = make_float2(f, f);
+        if (more) {
+          row_s = *(rp += rstep);
+          col_s = *(cp += cstep);
+        }
       }
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc) {
         uint32_t(&x)[CH] = v[cc & 1];
+        // the columns' scales, before the values are there: of the chunk's columns, or (FRAG) of the
+        // thread's four pairs of them
+        float2 f[CH / 2];
+        if constexpr (Cfg::FRAG) {
+#pragma unroll
+          for (int n = 0; n < 4; ++n) f[n] = *reinterpret_cast<const float2 *>(sc + cc * CH + 8 * n + 2 * (lane & 3));
+        } else if constexpr (Cfg::VEC) {
+#pragma unroll
+          for (int j = 0; j < CH; j += 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(sc + cc * CH + j);
+            f[j / 2] = __fmul2_rn(make_float2(u.x, u.y), rs[0]);
+            f[j / 2 + 1] = __fmul2_rn(make_float2(u.z, u.w), rs[0]);
+          }
+        }
         tmem_ld_wait_for(x);
         if (cc + 1 < NC) {
-          tmem_ld(src + b * Cfg::BN + (cc + 1) * CH, v[(cc + 1) & 1]);
+          tmem_ld_chunk<Cfg>(src + b * Cfg::BN + (cc + 1) * CH, v[(cc + 1) & 1]);
         } else {
           tc_fence_before_sync();
           __syncwarp();
@@ -500,46 +608,51 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
           }
           if (more) {
             if (!acc_ready(it + 1)) return;
-            tmem_ld(src + (it + 1) % Cfg::ACCS * Cfg::BN, v[0]);
+            tmem_ld_chunk<Cfg>(src + (it + 1) % Cfg::ACCS * Cfg::BN, v[0]);
           }
         }
 #pragma unroll
-        for (int j = 0; j < CH; j += 4) {
-          float2 a = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-          float2 c = make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
-          if constexpr (Cfg::VEC) {
-            const float4 f = *reinterpret_cast<const float4 *>(sc + cc * CH + j);
-            a = __fmul2_rn(a, make_float2(f.x, f.y));
-            c = __fmul2_rn(c, make_float2(f.z, f.w));
-          }
+        for (int j = 0; j < CH; j += 2) {
           float *o = acc + cc * CH + j;
-          const float2 o0 = __ffma2_rn(a, s2, make_float2(o[0], o[1]));
-          const float2 o1 = __ffma2_rn(c, s2, make_float2(o[2], o[3]));
-          o[0] = o0.x;
-          o[1] = o0.y;
-          o[2] = o1.x;
-          o[3] = o1.y;
+          const float2 a = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+          const float2 c = Cfg::FRAG  ? __fmul2_rn(f[j % 16 / 4], rs[j / 16 * 2 + j / 2 % 2])
+                           : Cfg::VEC ? f[j / 2]
+                                      : rs[0];
+          const float2 sum = __ffma2_rn(a, c, make_float2(o[0], o[1]));
+          o[0] = sum.x;
+          o[1] = sum.y;
         }
       }
       if constexpr (Cfg::VEC) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.sc_empty(it % Cfg::SCALE_SLOTS));
+        if (!more || i == SB - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.sc_empty(slot));
+          ++group;
+        }
       }
     }
     if (Cfg::GROUP == 1 && p.split > 1) {
       // every MMA of this CTA has completed, so the stage ring is free
+      if constexpr (Cfg::FRAG) {
 #pragma unroll
-      for (int j = 0; j < EC; j += 4)
-        sts128(sbase + 4 * (row * Cfg::PART_PITCH + half * EC + j),
-               make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
+        for (int j = 0; j < EC; j += 2) {
+          const int r = 32 * q + frag_row(j, lane), c = half * EC + frag_col(j, lane);
+          *reinterpret_cast<float2 *>(smem + 4 * (r * Cfg::PART_PITCH + c)) = make_float2(acc[j], acc[j + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < EC; j += 4)
+          sts128(sbase + 4 * (row * Cfg::PART_PITCH + half * EC + j),
+                 make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
+      }
     } else {
-      const int c = c0 + half * EC;
+      const int c = c0 + half * EC, r = r0 + (Cfg::FRAG ? 32 * q : row);
       if (p.typeC == SGEMM_TYPE_F32)
-        fp8_store<Cfg, float>(p, r0 + row, c, acc);
+        fp8_store<Cfg, float>(p, r, c, lane, acc);
       else if (p.typeC == SGEMM_TYPE_BF16)
-        fp8_store<Cfg, __nv_bfloat16>(p, r0 + row, c, acc);
+        fp8_store<Cfg, __nv_bfloat16>(p, r, c, lane, acc);
       else
-        fp8_store<Cfg, __half>(p, r0 + row, c, acc);
+        fp8_store<Cfg, __half>(p, r, c, lane, acc);
     }
   }
 }
