@@ -30,6 +30,8 @@ TYPE_F32, TYPE_BF16, TYPE_F16, TYPE_E4M3, TYPE_E5M2 = 0, 1, 2, 8, 9
 _FLOAT = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
 _FP8 = {torch.float8_e4m3fn: TYPE_E4M3, torch.float8_e5m2: TYPE_E5M2}
 _F32 = {torch.float32: TYPE_F32}
+_SAME = {code: {dtype: code} for dtype, code in _FLOAT.items()}
+_WEIGHT = {code: _F32 | same for code, same in _SAME.items()}   # a norm's weights: float32 or its input's type
 
 RmsNormFp8 = collections.namedtuple("RmsNormFp8", "q scale h y rstd")
 RmsNormFp8.__doc__ = """What rms_norm_fp8 returns: the quantised norm and its scales, h = x + residual
@@ -110,46 +112,54 @@ def sgemm_rms_norm_backward_workspace(rows, cols) -> int:
 
 # ------------------------------------------------------------------ torch
 def _mat(t, name, types):
-    """(pointer, rows, cols, ld, type) of a 2-D CUDA tensor with unit column stride."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in types:
-        raise TypeError(f"{name} must be a 2-D tensor of {' or '.join(str(d) for d in types)}")
-    if not t.is_cuda:
+    """(pointer, rows, cols, ld, type, device) of a 2-D CUDA tensor with unit column stride."""
+    try:
+        rows, cols = t.shape
+        ld, st1 = t.stride()
+        code = types[t.dtype]
+    except (AttributeError, KeyError, ValueError):
+        raise TypeError(f"{name} must be a 2-D tensor of {' or '.join(str(d) for d in types)}") from None
+    dev = t.get_device()
+    if dev < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    rows, cols = t.shape
-    ld, st1 = t.stride()
-    if cols > 1 and st1 != 1:
+    if st1 != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
     if ld < cols or ld < 1:
         if rows > 1:
             raise ValueError(f"{name} has overlapping rows")
         ld = cols if cols > 0 else 1
-    return t.data_ptr(), rows, cols, ld, types[t.dtype]
+    return t.data_ptr(), rows, cols, ld, code, dev
 
 
 def _vec(t, name, n, types):
-    """(pointer, type) of a contiguous 1-D CUDA tensor of n elements."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.dtype not in types:
-        raise TypeError(f"{name} must be a 1-D tensor of {' or '.join(str(d) for d in types)}")
-    if not t.is_cuda:
+    """(pointer, type, device) of a contiguous 1-D CUDA tensor of n elements."""
+    try:
+        (size,) = t.shape
+        code = types[t.dtype]
+    except (AttributeError, KeyError, ValueError):
+        raise TypeError(f"{name} must be a 1-D tensor of {' or '.join(str(d) for d in types)}") from None
+    dev = t.get_device()
+    if dev < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if size != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must hold {n} contiguous elements")
-    return t.data_ptr(), types[t.dtype]
+    return t.data_ptr(), code, dev
 
 
-def _same_device(first, *rest):
-    dev = first.get_device()
-    for t in rest:
-        if t is not None and t.get_device() != dev:
+def _one_device(*devs):
+    for d in devs:
+        if d != devs[0]:
             raise ValueError("tensors are on different devices")
-    return dev
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(stream, dev):
     """The context in which a call allocates and runs, or None if that is the current one."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return None if dev == _current_device() else torch.cuda.device(dev)
 
 
 def _cdiv(a, b):
@@ -172,12 +182,11 @@ def _fp8_type(dtype):
 def quantize_fp8(x, block=(1, BLOCK), dtype=torch.float8_e4m3fn, stream=None):
     """(q, scale) of a float32, bfloat16 or float16 matrix in blocks of (1, 128), (128, 1) or (128, 128):
     scale = max(max|x| / F, 2^-126) per block, q = x / scale rounded to `dtype`."""
-    px, rows, cols, ldx, tx = _mat(x, "x", _FLOAT)
+    px, rows, cols, ldx, tx, dev = _mat(x, "x", _FLOAT)
     tq = _fp8_type(dtype)
     br, bc = block
     if (br, bc) not in ((1, BLOCK), (BLOCK, 1), (BLOCK, BLOCK)):
         raise ValueError("block must be (1, 128), (128, 1) or (128, 128)")
-    dev = x.get_device()
     ctx = _on(stream, dev)
     if ctx is not None:
         with ctx:
@@ -194,9 +203,8 @@ def quantize_fp8(x, block=(1, BLOCK), dtype=torch.float8_e4m3fn, stream=None):
 
 def quantize_fp8_both(x, dtype=torch.float8_e4m3fn, stream=None):
     """(q_rows, scale_rows, q_cols, scale_cols): x in (1, 128) and in (128, 1) blocks, in one pass over it."""
-    px, rows, cols, ldx, tx = _mat(x, "x", _FLOAT)
+    px, rows, cols, ldx, tx, dev = _mat(x, "x", _FLOAT)
     tq = _fp8_type(dtype)
-    dev = x.get_device()
     ctx = _on(stream, dev)
     if ctx is not None:
         with ctx:
@@ -215,14 +223,15 @@ def quantize_fp8_both(x, dtype=torch.float8_e4m3fn, stream=None):
 
 
 def _scales(s, name, outer, kb, inner_rows):
-    """(pointer, ld, block) of an operand's scales; the block along the outer dimension follows from the shape."""
-    ps, r, c, ld, _ = _mat(s, name, _F32)
+    """(pointer, ld, block, device) of an operand's scales; the block along the outer dimension follows from the
+    shape."""
+    ps, r, c, ld, _, dev = _mat(s, name, _F32)
     o, k = (c, r) if inner_rows else (r, c)
     if k == kb:
         if o == outer:
-            return ps, ld, 1
-        if o == _cdiv(outer, BLOCK):
-            return ps, ld, BLOCK
+            return ps, ld, 1, dev
+        if o == (outer + 127) // 128:
+            return ps, ld, BLOCK, dev
     raise ValueError(f"{name} is {r} x {c}: one scale is wanted for each block of 128 along the inner dimension "
                      f"({kb}) times each 1 or 128 along the outer one ({outer} or {_cdiv(outer, BLOCK)})")
 
@@ -235,16 +244,17 @@ def gemm_fp8(A, A_scale, B, B_scale, C=None, alpha=1.0, beta=0.0, transA=False, 
     128 elements along K and per 1 or 128 along M or N.  C is float32, bfloat16 or float16; if it is None a new
     M x N tensor of ``out_dtype`` (default bfloat16) is returned (beta must then be 0).
     """
-    pa, ra, ca, lda, fa = _mat(A, "A", _FP8)
-    pb, rb, cb, ldb, fb = _mat(B, "B", _FP8)
+    pa, ra, ca, lda, fa, dev = _mat(A, "A", _FP8)
+    pb, rb, cb, ldb, fb, devb = _mat(B, "B", _FP8)
     M, K = (ca, ra) if transA else (ra, ca)
     Kb, N = (cb, rb) if transB else (rb, cb)
     if K != Kb:
         raise ValueError(f"inner dimensions differ: {K} vs {Kb}")
-    kb = _cdiv(K, BLOCK)
-    psa, ldsa, ba = _scales(A_scale, "A_scale", M, kb, transA)
-    psb, ldsb, bb = _scales(B_scale, "B_scale", N, kb, not transB)
-    dev = _same_device(A, A_scale, B, B_scale, C)
+    kb = (K + 127) // 128
+    psa, ldsa, ba, devsa = _scales(A_scale, "A_scale", M, kb, transA)
+    psb, ldsb, bb, devsb = _scales(B_scale, "B_scale", N, kb, not transB)
+    if not dev == devb == devsa == devsb:
+        raise ValueError("tensors are on different devices")
     ctx = _on(stream, dev)
     if ctx is not None:
         with ctx:
@@ -261,9 +271,10 @@ def gemm_fp8(A, A_scale, B, B_scale, C=None, alpha=1.0, beta=0.0, transA=False, 
     else:
         if out_dtype is not None and out_dtype != C.dtype:
             raise TypeError(f"C is {C.dtype}, out_dtype {out_dtype}")
-        pc, rc, cc, ldc, tc = _mat(C, "C", _FLOAT)
-        if (rc, cc) != (M, N):
+        pc, rc, cc, ldc, tc, devc = _mat(C, "C", _FLOAT)
+        if rc != M or cc != N:
             raise ValueError(f"C must be {M} x {N}")
+        _one_device(dev, devc)
     st = (_lib or _library()).sgemm_fp8(1 if transA else 0, 1 if transB else 0, M, N, K, alpha, pa, fa, lda, psa, ldsa,
                                         ba, pb, fb, ldb, psb, ldsb, bb, beta, pc, tc, ldc, _current_raw_stream(dev))
     if st != 0:
@@ -277,15 +288,16 @@ def rms_norm_fp8(x, weight, residual=None, eps=1e-6, dtype=torch.float8_e4m3fn, 
     h = x + residual in x's type (None without a residual: h is x).  With training=True also y, the norm in x's
     type, and rstd = 1 / sqrt(mean(h^2) + eps) per row, which rms_norm_backward wants.  `weight` is float32 or of
     x's type."""
-    px, rows, cols, ldx, tx = _mat(x, "x", _FLOAT)
+    px, rows, cols, ldx, tx, dev = _mat(x, "x", _FLOAT)
     tq = _fp8_type(dtype)
-    pw, tw = _vec(weight, "weight", cols, _F32 if x.dtype == torch.float32 else {torch.float32: TYPE_F32, x.dtype: tx})
-    dev = _same_device(x, weight, residual)
-    pr, ldr = None, 0
+    pw, tw, devw = _vec(weight, "weight", cols, _WEIGHT[tx])
+    pr, ldr, devr = None, 0, dev
     if residual is not None:
-        pr, rr, rc, ldr, _ = _mat(residual, "residual", {x.dtype: tx})
-        if (rr, rc) != (rows, cols):
+        pr, rr, rc, ldr, _, devr = _mat(residual, "residual", _SAME[tx])
+        if rr != rows or rc != cols:
             raise ValueError(f"residual must be {rows} x {cols}")
+    if not dev == devw == devr:
+        raise ValueError("tensors are on different devices")
     ctx = _on(stream, dev)
     if ctx is not None:
         with ctx:
@@ -313,19 +325,18 @@ def rms_norm_fp8(x, weight, residual=None, eps=1e-6, dtype=torch.float8_e4m3fn, 
 def rms_norm_backward(dy, h, weight, rstd, dh=None, stream=None):
     """(dx, dweight) of y = h * rstd * weight: dx (the gradient of x and of the residual alike, `dh` added to it)
     in h's type, dweight in weight's.  `dh` is the gradient that reaches h along the residual path."""
-    pd, rows, cols, lddy, tx = _mat(dy, "dy", _FLOAT)
-    own = {dy.dtype: tx}
-    ph, hr, hc, ldh, _ = _mat(h, "h", own)
-    if (hr, hc) != (rows, cols):
+    pd, rows, cols, lddy, tx, dev = _mat(dy, "dy", _FLOAT)
+    ph, hr, hc, ldh, _, devh = _mat(h, "h", _SAME[tx])
+    if hr != rows or hc != cols:
         raise ValueError(f"h must be {rows} x {cols}")
-    pw, tw = _vec(weight, "weight", cols, _F32 if tx == TYPE_F32 else {torch.float32: TYPE_F32, dy.dtype: tx})
-    pt, _ = _vec(rstd, "rstd", rows, _F32)
-    pg, lddh = None, 0
+    pw, tw, devw = _vec(weight, "weight", cols, _WEIGHT[tx])
+    pt, _, devt = _vec(rstd, "rstd", rows, _F32)
+    pg, lddh, devg = None, 0, dev
     if dh is not None:
-        pg, gr, gc, lddh, _ = _mat(dh, "dh", own)
-        if (gr, gc) != (rows, cols):
+        pg, gr, gc, lddh, _, devg = _mat(dh, "dh", _SAME[tx])
+        if gr != rows or gc != cols:
             raise ValueError(f"dh must be {rows} x {cols}")
-    dev = _same_device(dy, h, weight, rstd, dh)
+    _one_device(dev, devh, devw, devt, devg)
     ctx = _on(stream, dev)
     if ctx is not None:
         with ctx:
