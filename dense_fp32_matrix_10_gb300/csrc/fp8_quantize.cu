@@ -15,10 +15,25 @@ namespace {
 
 enum : int { kRow = 1, kCol = 2, kTile = 4 };
 
+// Maxima over 16 lanes of eight values each: a lane passes on the half of its values that the other
+// lane of a pair will own, so three exchanges leave one value a lane and a fourth joins the two lanes
+// that own the same one.  Lane l (of 16) ends with the maximum of value owned(l).
+__device__ __forceinline__ int owned(int lane16) { return (lane16 >> 3 & 1) * 4 + (lane16 >> 2 & 1) * 2 + (lane16 >> 1 & 1); }
+__device__ __forceinline__ float max_of_8x16(const float (&v)[8], int lane16) {
+  float a[4], b[2];
+  const bool h8 = lane16 & 8, h4 = lane16 & 4, h2 = lane16 & 2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = max_abs(h8 ? v[4 + i] : v[i], __shfl_xor_sync(~0u, h8 ? v[i] : v[4 + i], 8));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) b[i] = max_abs(h4 ? a[2 + i] : a[i], __shfl_xor_sync(~0u, h4 ? a[i] : a[2 + i], 4));
+  float c = max_abs(h2 ? b[1] : b[0], __shfl_xor_sync(~0u, h2 ? b[0] : b[1], 2));
+  return max_abs(c, __shfl_xor_sync(~0u, c, 1));
+}
+
 template <class T, int MODE>
-__global__ void __launch_bounds__(256) quantize_kernel(const QuantizeParams p, const int64_t tiles_c,
-                                                       const bool vec_x, const bool vec_r,
-                                                       const bool vec_c) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
+    quantize_kernel(const QuantizeParams p, const int64_t tiles_c, const bool vec_x, const bool vec_r,
+                    const bool vec_c) {
   __shared__ float part[8][128];   // column maxima of each warp, then of the tile
   griddep_wait();
   griddep_launch_dependents();
@@ -27,42 +42,45 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantizeParams p, c
   const int64_t c0 = tc * 128 + lane16 * 8;
   const int64_t left = p.cols - c0;
   const int n = left < 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
+  const int64_t r0 = tr * 128 + row16;   // this thread's rows: r0 + 16 i
+  const int rows = static_cast<int>(min(int64_t(128), p.rows - r0));
   Raw<T> raw[8];
+  {
+    const T *x = static_cast<const T *>(p.x) + r0 * p.ldx + c0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = tr * 128 + row16 + 16 * i;
-    raw[i] = load8(static_cast<const T *>(p.x) + (r < p.rows ? r * p.ldx + c0 : 0), r < p.rows ? n : 0, vec_x);
+    for (int i = 0; i < 8; ++i) raw[i] = load8(x + 16 * i * p.ldx, 16 * i < rows ? n : 0, vec_x);
   }
-  float cmax[8], tmax = 0.0f;
+  float cmax[8], rmax[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) cmax[j] = 0.0f;
+  for (int j = 0; j < 8; ++j) cmax[j] = rmax[j] = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float v[8];
     unpack(raw[i], v);
-    if (MODE & kCol) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cmax[j] = max_abs(cmax[j], v[j]);
+    for (int j = 0; j < 8; ++j) {
+      if (MODE & kCol) cmax[j] = max_abs(cmax[j], v[j]);
+      if (MODE & (kRow | kTile)) rmax[i] = max_abs(rmax[i], v[j]);
     }
-    if (MODE & (kRow | kTile)) {
-      float a = 0.0f;
+  }
+  if (MODE & kRow) {
+    // each lane divides for the row that it owns
+    const int mine = owned(lane16);
+    const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), inv = __fdiv_rn(1.0f, s);
+    if ((lane16 & 1) == 0 && 16 * mine < rows) p.sr[(r0 + 16 * mine) * p.ldsr + tc] = s;
+    unsigned char *q = p.qr + r0 * p.ldqr + c0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a = max_abs(a, v[j]);
-      if (MODE & kTile) {
-        tmax = max_abs(tmax, a);
-      } else {
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) a = max_abs(a, __shfl_xor_sync(~0u, a, d));
-        const float s = block_scale(a, p.e5m2);
-        const int64_t r = tr * 128 + row16 + 16 * i;
-        if (r < p.rows) {
-          store8_fp8(p.qr + r * p.ldqr + c0, to_fp8x8(v, __fdiv_rn(1.0f, s), p.e5m2), n, vec_r);
-          if (lane16 == 0) p.sr[r * p.ldsr + tc] = s;
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float f = __shfl_sync(~0u, inv, (i & 4) * 2 + (i & 2) * 2 + (i & 1) * 2, 16);
+      float v[8];
+      unpack(raw[i], v);
+      if (16 * i < rows) store8_fp8(q + 16 * i * p.ldqr, to_fp8x8(v, f, p.e5m2), n, vec_r);
     }
   }
   if (MODE & kTile) {
+    float tmax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tmax = max_abs(tmax, rmax[i]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) tmax = max_abs(tmax, __shfl_xor_sync(~0u, tmax, d));
     if ((threadIdx.x & 31) == 0) part[0][warp] = tmax;
@@ -73,10 +91,10 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantizeParams p, c
     if (threadIdx.x == 0) p.sr[tr * p.ldsr + tc] = s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t r = tr * 128 + row16 + 16 * i;
       float v[8];
       unpack(raw[i], v);
-      if (r < p.rows) store8_fp8(p.qr + r * p.ldqr + c0, to_fp8x8(v, inv, p.e5m2), n, vec_r);
+      if (16 * i < rows)
+        store8_fp8(p.qr + (r0 + 16 * i) * p.ldqr + c0, to_fp8x8(v, inv, p.e5m2), n, vec_r);
     }
   }
   if (MODE & kCol) {
@@ -102,12 +120,12 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantizeParams p, c
     for (int j = 0; j < 8; ++j) inv[j] = part[0][lane16 * 8 + j];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t r = tr * 128 + row16 + 16 * i;
       float v[8];
       unpack(raw[i], v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= inv[j];
-      if (r < p.rows) store8_fp8(p.qc + r * p.ldqc + c0, to_fp8x8(v, 1.0f, p.e5m2), n, vec_c);
+      if (16 * i < rows)
+        store8_fp8(p.qc + (r0 + 16 * i) * p.ldqc + c0, to_fp8x8(v, 1.0f, p.e5m2), n, vec_c);
     }
   }
 }

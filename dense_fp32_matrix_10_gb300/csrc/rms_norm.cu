@@ -8,9 +8,11 @@
 // its maximum is four shuffles.  A row of up to 8 * G * NV elements stays in
 // registers between the statistics and the output: x and r are read once.
 // Longer rows are walked in segments and read a second time.
+#include <mutex>
+
+#include "dispatch.h"
 #include "fp8.cuh"
 #include "fp8.h"
-#include "internal.h"
 
 namespace sg {
 namespace {
@@ -115,112 +117,190 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) rms_norm_kernel(const No
   }
 }
 
-// CTA b takes rows b, b + grid, ... and adds dy h t of its rows per column in
-// registers (LONG: in its row of the workspace).
-template <class T, int NV, bool LONG>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
-    rms_norm_backward_kernel(const NormGradParams p, const int vec) {
+// A thread's own 16 bytes from global to its own place in shared memory, asynchronously.
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most `n` of this thread's groups are in flight.
+__device__ __forceinline__ void copies_wait(int n) {
+  if (n <= 0)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// CTA b takes rows b, b + grid, ... and adds dy h t of its rows per column in registers.  A thread
+// copies its own elements of dy, h and dh of the next `depth` rows to places of its own in shared
+// memory and reads them there (no barrier but the sum's): bound by memory, it needs some 50 KB in
+// flight on every SM, and one row in registers at a time had none during the sum (4095 x 8192 bf16
+// 108 us; XXX so).
+template <class T, int NV>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 4 ? 1 : NV == 2 ? 2 : 1)
+    rms_norm_backward_kernel(const NormGradParams p, const int vec, const int depth) {
+  constexpr int U = sizeof(Raw<T>) / 16;   // 16-byte units of eight elements
+  extern __shared__ __align__(16) uint4 rows_smem[];   // [depth][dy, h, dh][NV][U][thread]
   __shared__ float red[2][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t seg = static_cast<int64_t>(8) * NV * blockDim.x, pitch = (p.cols + 7) / 8 * 8;
-  float dw[NV][8], dy[NV][8], h[NV][8], w[NV][8];
-  int turn = 0;
+  float dw[NV][8];
+  int turn = 0, n[NV];
+  const auto column = [&](int j) { return (static_cast<int64_t>(j) * blockDim.x + threadIdx.x) * 8; };
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    n[j] = static_cast<int>(max(int64_t(0), min(int64_t(8), p.cols - column(j))));
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
-  auto at = [&](int64_t base, int j, int &n) {
-    const int64_t c = base + (static_cast<int64_t>(j) * blockDim.x + threadIdx.x) * 8;
-    n = static_cast<int>(max(int64_t(0), min(int64_t(8), p.cols - c)));
-    return c;
+  }
+  const auto place = [&](int slot, int a, int j, int u) {
+    return rows_smem + (((slot * 3 + a) * NV + j) * U + u) * blockDim.x + threadIdx.x;
   };
-  auto load_weights = [&](int64_t base) {
+  const auto fetch = [&](int64_t row, int slot) {
+    if (row < p.rows) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      int n;
-      const int64_t c = at(base, j, n);
-      load_w<T>(p.w, p.w_f32, c, n, vec & 4, w[j]);
-    }
-  };
-  auto load = [&](int64_t row, int64_t base) {
+      for (int a = 0; a < 3; ++a) {
+        const T *x = static_cast<const T *>(a == 0 ? p.dy : a == 1 ? p.h : p.dh);
+        const int64_t ld = a == 0 ? p.lddy : a == 1 ? p.ldh : p.lddh;
+        if (a == 2 && !x) continue;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      int n;
-      const int64_t c = at(base, j, n);
-      unpack(load8(static_cast<const T *>(p.dy) + row * p.lddy + c, n, vec & 1), dy[j]);
-      unpack(load8(static_cast<const T *>(p.h) + row * p.ldh + c, n, vec & 2), h[j]);
+        for (int j = 0; j < NV; ++j) {
+          const T *src = x + row * ld + column(j);
+          if (n[j] == 8 && (vec >> a & 1)) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) copy16(place(slot, a, j, u), reinterpret_cast<const uint4 *>(src) + u);
+          } else {
+            const Raw<T> r = load8(src, n[j], false);
+#pragma unroll
+            for (int u = 0; u < U; ++u) *place(slot, a, j, u) = r.u[u];
+          }
+        }
+      }
     }
+    copies_commit();
   };
-  if (!LONG) load_weights(0);
+  const auto take = [&](int slot, int a, int j, float (&v)[8]) {
+    Raw<T> r;
+#pragma unroll
+    for (int u = 0; u < U; ++u) r.u[u] = *place(slot, a, j, u);
+    unpack(r, v);
+  };
+  for (int d = 0; d < depth; ++d) fetch(blockIdx.x + static_cast<int64_t>(d) * gridDim.x, d);
+  int slot = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    copies_wait(depth - 1);
     const float t = p.t[row];
     float sum = 0.0f;
-    for (int64_t base = 0; base < (LONG ? p.cols : 1); base += seg) {
-      load(row, base);
-      if (LONG) load_weights(base);
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      float d[8], x[8], w[8];
+      take(slot, 0, j, d);
+      take(slot, 1, j, x);
+      load_w<T>(p.w, p.w_f32, column(j), n[j], vec & 8, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += dy[j][i] * w[j][i] * h[j][i];
+      for (int i = 0; i < 8; ++i) {
+        sum += d[i] * w[i] * x[i];
+        dw[j][i] += d[i] * x[i] * t;
+      }
     }
     sum = row_sum(sum, red, turn);
     const float k = t * t * (sum / static_cast<float>(p.cols));
-    for (int64_t base = 0; base < (LONG ? p.cols : 1); base += seg) {
-      if (LONG) {
-        load(row, base);
-        load_weights(base);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float d[8], x[8], w[8], v[8];
+      take(slot, 0, j, d);
+      take(slot, 1, j, x);
+      if (p.dh) take(slot, 2, j, v);
+      load_w<T>(p.w, p.w_f32, column(j), n[j], vec & 8, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = t * (d[i] * w[i] - x[i] * k);
+        v[i] = p.dh ? v[i] + y : y;
       }
+      store8(static_cast<T *>(p.dx) + row * p.lddx + column(j), v, n[j], vec & 16);
+    }
+    fetch(row + static_cast<int64_t>(depth) * gridDim.x, slot);
+    slot = slot + 1 == depth ? 0 : slot + 1;
+  }
+  copies_wait(0);
+  if (!p.partial) return;
+  const int64_t pitch = (p.cols + 7) / 8 * 8;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        int n;
-        const int64_t c = at(base, j, n);
-        float v[8];
-        if (p.dh) unpack(load8(static_cast<const T *>(p.dh) + row * p.lddh + c, n, vec & 8), v);
+  for (int j = 0; j < NV; ++j)
+    if (n[j] > 0) store8(p.partial + blockIdx.x * pitch + column(j), dw[j], 8, true);
+}
+
+// Rows too long for registers: walked in segments, twice; the sums of dy h t are kept in this CTA's
+// row of the workspace.
+template <class T>
+__global__ void __launch_bounds__(512) rms_norm_backward_long_kernel(const NormGradParams p, const int vec) {
+  __shared__ float red[2][32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t pitch = (p.cols + 7) / 8 * 8, step = static_cast<int64_t>(8) * blockDim.x;
+  int turn = 0;
+  float dy[8], h[8], w[8];
+  const auto load = [&](int64_t row, int64_t c) {
+    const int n = static_cast<int>(min(int64_t(8), p.cols - c));
+    unpack(load8(static_cast<const T *>(p.dy) + row * p.lddy + c, n, vec & 1), dy);
+    unpack(load8(static_cast<const T *>(p.h) + row * p.ldh + c, n, vec & 2), h);
+    load_w<T>(p.w, p.w_f32, c, n, vec & 8, w);
+    return n;
+  };
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float t = p.t[row];
+    float sum = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < p.cols; c += step) {
+      load(row, c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float d = t * (dy[j][i] * w[j][i] - h[j][i] * k);
-          v[i] = p.dh ? v[i] + d : d;
-        }
-        store8(static_cast<T *>(p.dx) + row * p.lddx + c, v, n, vec & 16);
-        if (LONG && p.partial && n > 0) {   // this CTA's own row: no other thread touches these
-          float *mine = p.partial + blockIdx.x * pitch + c;
+      for (int i = 0; i < 8; ++i) sum += dy[i] * w[i] * h[i];
+    }
+    sum = row_sum(sum, red, turn);
+    const float k = t * t * (sum / static_cast<float>(p.cols));
+    for (int64_t c = threadIdx.x * 8; c < p.cols; c += step) {
+      const int n = load(row, c);
+      float v[8];
+      if (p.dh) unpack(load8(static_cast<const T *>(p.dh) + row * p.lddh + c, n, vec & 4), v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            mine[i] = (row == blockIdx.x ? 0.0f : mine[i]) + dy[j][i] * h[j][i] * t;
-        } else {
+      for (int i = 0; i < 8; ++i) {
+        const float d = t * (dy[i] * w[i] - h[i] * k);
+        v[i] = p.dh ? v[i] + d : d;
+      }
+      store8(static_cast<T *>(p.dx) + row * p.lddx + c, v, n, vec & 16);
+      if (p.partial) {   // no other thread touches these
+        float *mine = p.partial + blockIdx.x * pitch + c;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dw[j][i] += dy[j][i] * h[j][i] * t;
-        }
+        for (int i = 0; i < 8; ++i) mine[i] = (row == blockIdx.x ? 0.0f : mine[i]) + dy[i] * h[i] * t;
       }
     }
   }
-  if (LONG || !p.partial) return;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    int n;
-    const int64_t c = at(0, j, n);
-    if (n > 0) store8(p.partial + blockIdx.x * pitch + c, dw[j], 8, true);
-  }
 }
 
-// dw[c] = sum over the CTAs' partial rows, in their order.
+// dw[c] = sum over the CTAs' partial rows, in a fixed order: every 32nd of them by one thread (their
+// loads all in flight), then the 32 sums.
 template <class T>
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float *partial, int parts, int64_t cols, T *dw) {
-  __shared__ float red[8][32];
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, int parts, int64_t cols, T *dw) {
+  constexpr int PER = (kNormPartials + 31) / 32;
+  __shared__ float red[32][33];
   griddep_wait();
   const int64_t pitch = (cols + 7) / 8 * 8;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-  float v = 0.0f;
-  if (c < cols)
-    for (int i = threadIdx.y; i < parts; i += 8) v += partial[i * pitch + c];
-  red[threadIdx.y][threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.y == 0 && c < cols) {
+  float v[PER], sum = 0.0f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += red[i][threadIdx.x];
-    from_float(dw + c, v);
+  for (int i = 0; i < PER; ++i) {
+    const int r = threadIdx.y + 32 * i;
+    v[i] = c < cols && r < parts ? partial[r * pitch + c] : 0.0f;
   }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sum += v[i];
+  red[threadIdx.y][threadIdx.x] = sum;
+  __syncthreads();
+  sum = warp_sum(red[threadIdx.x][threadIdx.y]);
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && o < cols) from_float(dw + o, sum);
 }
 
 // Threads of a row and chunks of eight a thread holds.
@@ -256,6 +336,24 @@ cudaError_t norm_typed(const NormParams &p, int sm_count, cudaStream_t s) {
   return g.nv == 2 ? go(rms_norm_kernel<T, 2, false>) : go(rms_norm_kernel<T, 4, false>);
 }
 
+// Rows in flight per CTA: as many as fit in the shared memory of an SM shared by two CTAs, or (rows
+// of more than 34 KB in the three operands) taken whole by one.
+template <class T, int NV>
+cudaError_t launch_backward(const NormGradParams &p, dim3 grid, dim3 block, int vec, cudaStream_t s) {
+  const int row_bytes = 3 * NV * static_cast<int>(block.x) * static_cast<int>(sizeof(Raw<T>));
+  const int room = 2 * row_bytes <= 112 * 1024 && NV < 4 ? 112 * 1024 : 224 * 1024;
+  const int depth = room / row_bytes < 4 ? room / row_bytes : 4;
+  if (depth < 1) return cudaErrorInvalidConfiguration;
+  static std::once_flag once[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [] {
+    cudaFuncSetAttribute(rms_norm_backward_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+  });
+  return launch_maybe_pdl(rms_norm_backward_kernel<T, NV>, grid, block, static_cast<size_t>(depth) * row_bytes, s, true,
+                          p, vec, depth);
+}
+
 template <class T>
 cudaError_t backward_typed(const NormGradParams &p, int sm_count, cudaStream_t s) {
   RowShape g = row_shape(p.rows, p.cols, sm_count);
@@ -263,19 +361,19 @@ cudaError_t backward_typed(const NormGradParams &p, int sm_count, cudaStream_t s
   const int64_t ctas = p.rows < kNormPartials ? p.rows : kNormPartials;
   const int e = sizeof(T);
   const int vec = (aligned_rows(p.dy, p.lddy, e, 16) ? 1 : 0) | (aligned_rows(p.h, p.ldh, e, 16) ? 2 : 0) |
-                  (aligned_rows(p.w, 0, 4, 16) ? 4 : 0) | (p.dh && aligned_rows(p.dh, p.lddh, e, 16) ? 8 : 0) |
+                  (p.dh && aligned_rows(p.dh, p.lddh, e, 16) ? 4 : 0) | (aligned_rows(p.w, 0, 4, 16) ? 8 : 0) |
                   (aligned_rows(p.dx, p.lddx, e, 16) ? 16 : 0);
   const dim3 grid(static_cast<unsigned>(ctas)), block(g.threads);
-  auto go = [&](auto kernel) { return launch_maybe_pdl(kernel, grid, block, 0, s, true, p, vec); };
   if (ctas > 0) {
-    const cudaError_t err = g.loop       ? go(rms_norm_backward_kernel<T, 4, true>)
-                            : g.nv == 1  ? go(rms_norm_backward_kernel<T, 1, false>)
-                            : g.nv == 2  ? go(rms_norm_backward_kernel<T, 2, false>)
-                                         : go(rms_norm_backward_kernel<T, 4, false>);
+    const cudaError_t err =
+        g.loop      ? launch_maybe_pdl(rms_norm_backward_long_kernel<T>, grid, block, 0, s, true, p, vec)
+        : g.nv == 1 ? launch_backward<T, 1>(p, grid, block, vec, s)
+        : g.nv == 2 ? launch_backward<T, 2>(p, grid, block, vec, s)
+                    : launch_backward<T, 4>(p, grid, block, vec, s);
     if (err != cudaSuccess) return err;
   }
   if (!p.dw) return cudaSuccess;
-  const dim3 dgrid(static_cast<unsigned>((p.cols + 31) / 32)), dblock(32, 8);
+  const dim3 dgrid(static_cast<unsigned>((p.cols + 31) / 32)), dblock(32, 32);
   const int parts = static_cast<int>(ctas);
   if (p.w_f32)
     return launch_maybe_pdl(norm_dw_kernel<float>, dgrid, dblock, 0, s, true, p.partial, parts, p.cols,
