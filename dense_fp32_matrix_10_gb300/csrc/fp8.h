@@ -62,8 +62,8 @@ struct NormParams {
 };
 cudaError_t launch_rms_norm(const NormParams &p, int sm_count, cudaStream_t s);
 
-// At most this many CTAs of the backward kernel hold a partial sum of dw.
-constexpr int kNormPartials = 304;
+// CTAs of the backward kernel, each with a partial sum of dw, at most (for any type).
+int64_t norm_partials(int64_t rows, int64_t cols);
 struct NormGradParams {
   const void *dy, *h, *w, *dh;
   const float *t;
@@ -72,6 +72,6 @@ struct NormGradParams {
   int64_t lddy, ldh, lddh, lddx, rows, cols;
   int typeX, w_f32;
 };
-cudaError_t launch_rms_norm_backward(const NormGradParams &p, int sm_count, cudaStream_t s);
+cudaError_t launch_rms_norm_backward(const NormGradParams &p, cudaStream_t s);
 
 }  // namespace sg

@@ -234,8 +234,7 @@ sgemm_status_t sgemm_rms_norm_fp8(int64_t rows, int64_t cols, float eps, const v
 
 size_t sgemm_rms_norm_backward_workspace(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || !good_dim(rows) || !good_dim(cols)) return 0;
-  const int64_t parts = rows < kNormPartials ? rows : kNormPartials;
-  return static_cast<size_t>(parts) * static_cast<size_t>((cols + 7) / 8 * 8) * sizeof(float);
+  return static_cast<size_t>(norm_partials(rows, cols)) * static_cast<size_t>((cols + 7) / 8 * 8) * sizeof(float);
 }
 
 sgemm_status_t sgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *DY, int64_t lddy, const void *H,
@@ -265,8 +264,7 @@ sgemm_status_t sgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *D
   const sgemm_status_t st = check_ranges(r, 8);
   if (st != SGEMM_SUCCESS) return st;
   sgemm_status_t why = SGEMM_SUCCESS;
-  DeviceState *d = device_state(&why);
-  if (!d) return why;
+  if (!device_state(&why)) return why;
   NormGradParams p = {};
   p.dy = DY;
   p.h = H;
@@ -284,7 +282,7 @@ sgemm_status_t sgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *D
   p.cols = cols;
   p.typeX = typeX;
   p.w_f32 = typeW == SGEMM_TYPE_F32;
-  return queued(launch_rms_norm_backward(p, d->sm_count, reinterpret_cast<cudaStream_t>(stream)),
+  return queued(launch_rms_norm_backward(p, reinterpret_cast<cudaStream_t>(stream)),
                 (rows > 0 ? 1 : 0) + (DW ? 1 : 0));
 }
 

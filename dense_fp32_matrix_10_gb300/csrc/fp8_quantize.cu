@@ -31,7 +31,7 @@ __device__ __forceinline__ float max_of_8x16(const float (&v)[8], int lane16) {
 }
 
 template <class T, int MODE>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 && MODE != (kRow | kCol) ? 3 : 2)
     quantize_kernel(const QuantizeParams p, const int64_t tiles_c, const bool vec_x, const bool vec_r,
                     const bool vec_c) {
   __shared__ float part[8][128];   // column maxima of each warp, then of the tile

@@ -140,7 +140,7 @@ __device__ __forceinline__ void copies_wait(int n) {
 // flight on every SM, and one row in registers at a time had none during the sum (4095 x 8192 bf16
 // 108 us; XXX so).
 template <class T, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 4 ? 1 : NV == 2 ? 2 : 1)
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 2 ? 2 : 1)
     rms_norm_backward_kernel(const NormGradParams p, const int vec, const int depth) {
   constexpr int U = sizeof(Raw<T>) / 16;   // 16-byte units of eight elements
   extern __shared__ __align__(16) uint4 rows_smem[];   // [depth][dy, h, dh][NV][U][thread]
@@ -190,19 +190,22 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 4 ? 1 : NV == 2 ? 
   };
   for (int d = 0; d < depth; ++d) fetch(blockIdx.x + static_cast<int64_t>(d) * gridDim.x, d);
   int slot = 0;
+  float t_next = p.t[blockIdx.x];
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     copies_wait(depth - 1);
-    const float t = p.t[row];
-    float sum = 0.0f;
+    const float t = t_next;
+    if (row + gridDim.x < p.rows) t_next = p.t[row + gridDim.x];
+    float g[NV][8], sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float d[8], x[8], w[8];
+      float d[8], x[8];
       take(slot, 0, j, d);
       take(slot, 1, j, x);
-      load_w<T>(p.w, p.w_f32, column(j), n[j], vec & 8, w);
+      load_w<T>(p.w, p.w_f32, column(j), n[j], vec & 8, g[j]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sum += d[i] * w[i] * x[i];
+        g[j][i] *= d[i];
+        sum += g[j][i] * x[i];
         dw[j][i] += d[i] * x[i] * t;
       }
     }
@@ -210,14 +213,12 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 4 ? 1 : NV == 2 ? 
     const float k = t * t * (sum / static_cast<float>(p.cols));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float d[8], x[8], w[8], v[8];
-      take(slot, 0, j, d);
+      float x[8], v[8];
       take(slot, 1, j, x);
       if (p.dh) take(slot, 2, j, v);
-      load_w<T>(p.w, p.w_f32, column(j), n[j], vec & 8, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float y = t * (d[i] * w[i] - x[i] * k);
+        const float y = t * (g[j][i] - x[i] * k);
         v[i] = p.dh ? v[i] + y : y;
       }
       store8(static_cast<T *>(p.dx) + row * p.lddx + column(j), v, n[j], vec & 16);
@@ -279,23 +280,22 @@ __global__ void __launch_bounds__(512) rms_norm_backward_long_kernel(const NormG
   }
 }
 
-// dw[c] = sum over the CTAs' partial rows, in a fixed order: every 32nd of them by one thread (their
-// loads all in flight), then the 32 sums.
+// dw[c] = sum over the CTAs' partial rows, in a fixed order: every 32nd of them by one thread (ten
+// loads in flight), then the 32 sums.
 template <class T>
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, int parts, int64_t cols, T *dw) {
-  constexpr int PER = (kNormPartials + 31) / 32;
   __shared__ float red[32][33];
   griddep_wait();
   const int64_t pitch = (cols + 7) / 8 * 8;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-  float v[PER], sum = 0.0f;
+  float sum = 0.0f;
+  for (int r0 = threadIdx.y; r0 < parts; r0 += 320) {
+    float v[10];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int r = threadIdx.y + 32 * i;
-    v[i] = c < cols && r < parts ? partial[r * pitch + c] : 0.0f;
+    for (int i = 0; i < 10; ++i) v[i] = c < cols && r0 + 32 * i < parts ? partial[(r0 + 32 * i) * pitch + c] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) sum += v[i];
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) sum += v[i];
   red[threadIdx.y][threadIdx.x] = sum;
   __syncthreads();
   sum = warp_sum(red[threadIdx.x][threadIdx.y]);
@@ -336,40 +336,65 @@ cudaError_t norm_typed(const NormParams &p, int sm_count, cudaStream_t s) {
   return g.nv == 2 ? go(rms_norm_kernel<T, 2, false>) : go(rms_norm_kernel<T, 4, false>);
 }
 
-// Rows in flight per CTA: as many as fit in the shared memory of an SM shared by two CTAs, or (rows
-// of more than 34 KB in the three operands) taken whole by one.
+// The backward kernel's threads and chunks a thread, and the CTAs that share an SM (about 1024 threads;
+// the 4-chunk form's registers allow one).
+struct GradShape {
+  int threads, nv, per_sm;
+};
+GradShape grad_shape(int64_t cols, int elem) {
+  const int64_t chunks = (cols + 7) / 8;
+  GradShape g = {512, 0, 2};   // nv 0: rows longer than the registers hold
+  if (chunks <= 256 || (elem == 4 && chunks <= 1024))
+    g = {static_cast<int>((chunks + 31) / 32 * 32), 1, 0};
+  else if (chunks <= 1024)
+    g = {static_cast<int>(((chunks + 1) / 2 + 31) / 32 * 32), 2, 0};
+  else if (chunks <= 2048)
+    return {static_cast<int>(((chunks + 3) / 4 + 31) / 32 * 32), 4, 1};
+  if (g.nv > 0) g.per_sm = 1024 / g.threads < 8 ? (1024 / g.threads > 1 ? 1024 / g.threads : 1) : 8;
+  return g;
+}
+constexpr int kSms = 152;   // of a GB300: sizes the partial sums, whose number must not depend on the device
+int64_t grad_ctas(int64_t rows, const GradShape &g) {
+  const int64_t most = static_cast<int64_t>(kSms) * g.per_sm;
+  return rows < most ? rows : most;
+}
+
+// Rows in flight per CTA: up to four, as far as the CTAs of an SM find room in its shared memory.
 template <class T, int NV>
-cudaError_t launch_backward(const NormGradParams &p, dim3 grid, dim3 block, int vec, cudaStream_t s) {
-  const int row_bytes = 3 * NV * static_cast<int>(block.x) * static_cast<int>(sizeof(Raw<T>));
-  const int room = 2 * row_bytes <= 112 * 1024 && NV < 4 ? 112 * 1024 : 224 * 1024;
-  const int depth = room / row_bytes < 4 ? room / row_bytes : 4;
-  if (depth < 1) return cudaErrorInvalidConfiguration;
+cudaError_t launch_backward(const NormGradParams &p, const GradShape &g, int vec, cudaStream_t s) {
+  const int row_bytes = 3 * NV * g.threads * static_cast<int>(sizeof(Raw<T>));
+  const int fit = 224 * 1024 / g.per_sm / row_bytes;
+  const int depth = fit < 1 ? 1 : fit < 4 ? fit : 4;
   static std::once_flag once[kMaxDevices];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::call_once(once[dev], [] {
     cudaFuncSetAttribute(rms_norm_backward_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
   });
-  return launch_maybe_pdl(rms_norm_backward_kernel<T, NV>, grid, block, static_cast<size_t>(depth) * row_bytes, s, true,
-                          p, vec, depth);
+  return launch_maybe_pdl(rms_norm_backward_kernel<T, NV>, dim3(static_cast<unsigned>(grad_ctas(p.rows, g))),
+                          dim3(g.threads), static_cast<size_t>(depth) * row_bytes, s, true, p, vec, depth);
 }
 
 template <class T>
-cudaError_t backward_typed(const NormGradParams &p, int sm_count, cudaStream_t s) {
-  RowShape g = row_shape(p.rows, p.cols, sm_count);
-  if (g.threads == 32 && g.rows > 1) g = {32, g.nv, 1, false};   // one row at a time a CTA
-  const int64_t ctas = p.rows < kNormPartials ? p.rows : kNormPartials;
+cudaError_t backward_typed(const NormGradParams &p, cudaStream_t s) {
+  const GradShape g = grad_shape(p.cols, sizeof(T));
+  const int64_t ctas = grad_ctas(p.rows, g);
   const int e = sizeof(T);
   const int vec = (aligned_rows(p.dy, p.lddy, e, 16) ? 1 : 0) | (aligned_rows(p.h, p.ldh, e, 16) ? 2 : 0) |
                   (p.dh && aligned_rows(p.dh, p.lddh, e, 16) ? 4 : 0) | (aligned_rows(p.w, 0, 4, 16) ? 8 : 0) |
                   (aligned_rows(p.dx, p.lddx, e, 16) ? 16 : 0);
-  const dim3 grid(static_cast<unsigned>(ctas)), block(g.threads);
   if (ctas > 0) {
-    const cudaError_t err =
-        g.loop      ? launch_maybe_pdl(rms_norm_backward_long_kernel<T>, grid, block, 0, s, true, p, vec)
-        : g.nv == 1 ? launch_backward<T, 1>(p, grid, block, vec, s)
-        : g.nv == 2 ? launch_backward<T, 2>(p, grid, block, vec, s)
-                    : launch_backward<T, 4>(p, grid, block, vec, s);
+    cudaError_t err;
+    if constexpr (sizeof(T) == 4) {   // two chunks a thread: 16-bit rows only
+      err = cudaErrorInvalidConfiguration;
+    } else {
+      if (g.nv == 2) err = launch_backward<T, 2>(p, g, vec, s);
+    }
+    if (g.nv == 1) err = launch_backward<T, 1>(p, g, vec, s);
+    if (g.nv == 4) err = launch_backward<T, 4>(p, g, vec, s);
+    if (g.nv == 0)
+      err = launch_maybe_pdl(rms_norm_backward_long_kernel<T>, dim3(static_cast<unsigned>(ctas)), dim3(g.threads), 0, s,
+                             true, p, vec);
     if (err != cudaSuccess) return err;
   }
   if (!p.dw) return cudaSuccess;
@@ -392,11 +417,16 @@ cudaError_t launch_rms_norm(const NormParams &p, int sm_count, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_rms_norm_backward(const NormGradParams &p, int sm_count, cudaStream_t s) {
+int64_t norm_partials(int64_t rows, int64_t cols) {
+  const int64_t a = grad_ctas(rows, grad_shape(cols, 2)), b = grad_ctas(rows, grad_shape(cols, 4));
+  return a > b ? a : b;
+}
+
+cudaError_t launch_rms_norm_backward(const NormGradParams &p, cudaStream_t s) {
   switch (p.typeX) {
-    case SGEMM_TYPE_F32: return backward_typed<float>(p, sm_count, s);
-    case SGEMM_TYPE_BF16: return backward_typed<__nv_bfloat16>(p, sm_count, s);
-    default: return backward_typed<__half>(p, sm_count, s);
+    case SGEMM_TYPE_F32: return backward_typed<float>(p, s);
+    case SGEMM_TYPE_BF16: return backward_typed<__nv_bfloat16>(p, s);
+    default: return backward_typed<__half>(p, s);
   }
 }
 
