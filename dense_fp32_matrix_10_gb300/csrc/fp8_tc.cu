@@ -135,7 +135,8 @@ using Pair = Fp8Tc<2, 256, false, false, 6, 1>;      // 256 x 256 on two SMs
 using PairVec = Fp8Tc<2, 256, false, true, 6, 1>;
 using Tile = Fp8Tc<1, 128, false, false, 3, 2>;      // 128 x 128, two CTAs an SM
 using TileVec = Fp8Tc<1, 128, false, true, 3, 2>;
-using Narrow = Fp8Tc<1, 64, false, true, 4, 2>;      // up to 64 columns of C
+using Half = Fp8Tc<1, 64, false, false, 3, 2>;       // 128 x 64
+using HalfVec = Fp8Tc<1, 64, false, true, 3, 2>;
 using Few16 = Fp8Tc<1, 16, true, true, 5, 2>;        // up to 16, 32, 64 rows of C (its columns are the
 using Few32 = Fp8Tc<1, 32, true, true, 5, 2>;        // tile's rows)
 using Few64 = Fp8Tc<1, 64, true, true, 4, 2>;
@@ -144,11 +145,20 @@ bool tma_readable(const Fp8Operand &x, int64_t stored_rows) {
   return reinterpret_cast<uintptr_t>(x.q) % 16 == 0 && (x.ld % 16 == 0 || stored_rows == 1);
 }
 
-// CTAs per tile: as many as keep every CTA resident and give each at least two blocks.
-int pick_split(int64_t tiles, int64_t kblocks, int64_t slots) {
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= slots && kblocks >= 4 * split) split *= 2;
-  return split;
+int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Cycles that a product of `tiles` tiles of 128 x cols takes with `split` CTAs a tile, two CTAs an SM, as
+// measured: 920 for a block of k (the copies from the L2 cache bound either width), 4000 for a CTA's first
+// copies and its stores, and the exchange of partial tiles.
+int64_t tile_cycles(int64_t tiles, int64_t kblocks, int cols, int split, int64_t slots) {
+  return cdiv64(tiles * split, slots) * (cdiv64(kblocks, split) * 920 + 4000 + (split > 1 ? 1500 + 40 * cols : 0));
+}
+// CTAs per tile that make that least, each with two blocks or more.
+int pick_split(int64_t tiles, int64_t kblocks, int cols, int64_t slots) {
+  int best = 1;
+  for (int split = 2; split <= 8 && kblocks >= 2 * split; split *= 2)
+    if (tile_cycles(tiles, kblocks, cols, split, slots) < tile_cycles(tiles, kblocks, cols, best, slots)) best = split;
+  return best;
 }
 
 }  // namespace
@@ -158,18 +168,21 @@ bool fp8_tc_eligible(const Fp8Params &p) {
 }
 
 cudaError_t launch_fp8_tc(const Fp8Params &p, int sm_count, cudaStream_t s) {
-  const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  const int64_t kb = cdiv(p.K, 128), slots = 2 * sm_count;
+  const int64_t kb = cdiv64(p.K, 128), slots = 2 * sm_count;
   if (p.M <= 64 && !p.a.inner_rows) {
-    const int split = pick_split(cdiv(p.N, 128), kb, slots);
-    if (p.M <= 16) return launch<Few16>(p, split, s);
-    return p.M <= 32 ? launch<Few32>(p, split, s) : launch<Few64>(p, split, s);
+    const int64_t tiles = cdiv64(p.N, 128);
+    if (p.M <= 16) return launch<Few16>(p, pick_split(tiles, kb, 16, slots), s);
+    if (p.M <= 32) return launch<Few32>(p, pick_split(tiles, kb, 32, slots), s);
+    return launch<Few64>(p, pick_split(tiles, kb, 64, slots), s);
   }
-  if (p.N <= 64 && !p.b.inner_rows) return launch<Narrow>(p, pick_split(cdiv(p.M, 128), kb, slots), s);
-  const int64_t pairs = cdiv(p.M, 256) * cdiv(p.N, 256), tiles = cdiv(p.M, 128) * cdiv(p.N, 128);
   const bool vec = p.b.shift == 0;
-  if (pairs * 2 >= sm_count) return vec ? launch<PairVec>(p, 1, s) : launch<Pair>(p, 1, s);
-  const int split = pick_split(tiles, kb, slots);
+  const int64_t tiles = cdiv64(p.M, 128) * cdiv64(p.N, 128), halves = cdiv64(p.M, 128) * cdiv64(p.N, 64);
+  const int split = pick_split(tiles, kb, 128, slots), split_half = pick_split(halves, kb, 64, slots);
+  const int64_t tile = tile_cycles(tiles, kb, 128, split, slots), half = tile_cycles(halves, kb, 64, split_half, slots);
+  // a pair of SMs takes as long for a block of its 256 x 256 tile as two CTAs for one of theirs each
+  const int64_t pair = cdiv64(cdiv64(p.M, 256) * cdiv64(p.N, 256), sm_count / 2) * (kb * 920 + 3000);
+  if (pair <= tile && pair <= half) return vec ? launch<PairVec>(p, 1, s) : launch<Pair>(p, 1, s);
+  if (half < tile) return vec ? launch<HalfVec>(p, split_half, s) : launch<Half>(p, split_half, s);
   return vec ? launch<TileVec>(p, split, s) : launch<Tile>(p, split, s);
 }
 

@@ -61,7 +61,10 @@ template <int GROUP_, int BN_, bool SWAP_, bool VEC_, int STAGES_, int CTAS_>
 struct Fp8Tc {
   static constexpr int GROUP = GROUP_, BN = BN_, STAGES = STAGES_, CTAS = CTAS_;
   static constexpr bool SWAP = SWAP_, VEC = VEC_;
-  static constexpr int ROW_BYTES = 128 * 128, COL_BYTES = BN / GROUP * 128;
+  // (a tile of 64 columns takes the room of 128: of an outer-contiguous operand whole 128-byte rows are
+  // copied, and it uses one half of them)
+  static constexpr bool HALF_ROWS = BN == 64 && !SWAP_;
+  static constexpr int ROW_BYTES = 128 * 128, COL_BYTES = (HALF_ROWS ? 128 : BN / GROUP) * 128;
   static constexpr int STAGE_BYTES = ROW_BYTES + COL_BYTES;
   static constexpr int ACCS = BN >= 128 ? 2 : BN == 64 ? 4 : 8;   // accumulators
   static constexpr int TMEM_COLS = ACCS * BN;
@@ -84,7 +87,7 @@ struct Fp8Tc {
   static constexpr int BAR_OFFSET = SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 2 * SCALE_SLOTS + 1;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;
-  static_assert(VEC || BN % 128 == 0, "one scale per 128 columns needs whole blocks");
+  static_assert(VEC || BN % 64 == 0, "a thread's columns lie in one block of 128");
   static_assert(SMEM_BYTES * CTAS + CTAS * 1024 <= 233472, "shared memory over the SM's limit");
   static_assert(TMEM_COLS * CTAS <= 512, "tensor memory over the SM's limit");
   // ECOLS = 128: 128 sums and two chunks of 32 in flight per epilogue thread
@@ -93,10 +96,12 @@ struct Fp8Tc {
   static constexpr int SPLIT_TOTAL = 128 * REGS_WG0 + 32 * EPI_WARPS * REGS_EPI;
   static_assert(!SPLIT_REGS || SPLIT_TOTAL <= THREADS * ((65536 / CTAS / THREADS) & ~7),
                 "register split exceeds the launch budget");
-  // a cluster's partial tiles, [row][column], in the stage ring; the pitch is an odd number of 16-byte
-  // units, so that 8 rows of one column group lie in 8 different ones
-  static constexpr int PART_PITCH = BN + 4;
-  static_assert(GROUP == 2 || 128 * PART_PITCH * 4 <= STAGES * STAGE_BYTES, "partial tile does not fit");
+  // a cluster's partial tiles, in the stage ring: lines along C's rows ([row][column], SWAP [column][row]),
+  // so that a warp's reads of another CTA's are whole stretches of 64 bytes and more (16 bytes here and
+  // there took 3600 cycles instead of XXX at 24 x 8192 x 4096).  The [row][column] pitch is an odd number of
+  // 16-byte units: eight rows written at once lie in eight different ones.
+  static constexpr int PART_LINES = SWAP ? BN : 128, PART_PITCH = SWAP ? 128 : BN + 4;
+  static_assert(GROUP == 2 || PART_LINES * PART_PITCH * 4 <= STAGES * STAGE_BYTES, "partial tile does not fit");
 };
 
 template <class Cfg>
@@ -269,7 +274,7 @@ __device__ __forceinline__ void fp8_produce(const Fp8TcParams &p, const CUtensor
       const uint32_t st = sbase + s * Cfg::STAGE_BYTES;
       const int k0 = kb * 128;
       const int rx = p.row_inner ? r0 : k0, ry = p.row_inner ? k0 : r0;
-      const int cx = p.col_inner ? c0 : k0, cy = p.col_inner ? k0 : c0;
+      const int cx = p.col_inner ? (Cfg::HALF_ROWS ? c0 & ~127 : c0) : k0, cy = p.col_inner ? k0 : c0;
       if constexpr (Cfg::GROUP == 2) {
         // both CTAs' copies are counted on the even CTA's barrier
         if (rank == 0) mbar_arrive_expect_tx(bar.full(s), 2 * Cfg::STAGE_BYTES);
@@ -277,7 +282,8 @@ __device__ __forceinline__ void fp8_produce(const Fp8TcParams &p, const CUtensor
         tma_load_2d_pair(st, tm_row, full, rx, ry);
         tma_load_2d_pair(st + Cfg::ROW_BYTES, tm_col, full, cx, cy);
       } else {
-        mbar_arrive_expect_tx(bar.full(s), Cfg::STAGE_BYTES);
+        mbar_arrive_expect_tx(bar.full(s), Cfg::HALF_ROWS && !p.col_inner ? Cfg::ROW_BYTES + Cfg::COL_BYTES / 2
+                                                                         : Cfg::STAGE_BYTES);
         tma_load_2d(st, tm_row, bar.full(s), rx, ry);
         tma_load_2d(st + Cfg::ROW_BYTES, tm_col, bar.full(s), cx, cy);
       }
@@ -298,6 +304,12 @@ __device__ __forceinline__ void fp8_issue(const Fp8TcParams &p, uint32_t sbase, 
   uint32_t it = 0;
   bool ok = true;
   for (int t = w.first; t < p.num_tiles && ok; t += w.step) {
+    uint32_t col_off = Cfg::ROW_BYTES;   // of the tile's columns in a stage
+    if (Cfg::HALF_ROWS && p.col_inner) {
+      int r0, c0;
+      fp8_tile<Cfg>(p, t, 0, r0, c0);
+      col_off += c0 & 64;
+    }
     for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
       const uint32_t b = it % Cfg::ACCS, use = it / Cfg::ACCS;
       const uint32_t s = it % Cfg::STAGES, round = it / Cfg::STAGES;
@@ -309,7 +321,7 @@ __device__ __forceinline__ void fp8_issue(const Fp8TcParams &p, uint32_t sbase, 
       const uint32_t st = sbase + s * Cfg::STAGE_BYTES, d = tmem + b * Cfg::BN;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_fp8<Cfg::GROUP>(d, desc_fp8(st + kk * row_step), desc_fp8(st + Cfg::ROW_BYTES + kk * col_step), p.idesc,
+        mma_fp8<Cfg::GROUP>(d, desc_fp8(st + kk * row_step), desc_fp8(st + col_off + kk * col_step), p.idesc,
                             kk > 0);
       if constexpr (Cfg::GROUP == 2) {
         mma_commit_pair(bar.empty(s), 0x3);
@@ -430,6 +442,26 @@ __device__ __forceinline__ void fp8_put2(const Fp8TcParams &p, T *c, float v0, f
   else
     *reinterpret_cast<uint32_t *>(c) = pack2(v0, v1, T());
 }
+// The first n (of four, or more) consecutive elements of a row of C, at a multiple of four.
+template <class T>
+__device__ __forceinline__ void fp8_put4(const Fp8TcParams &p, T *c, float4 v, int n) {
+  float o[4] = {p.alpha * v.x, p.alpha * v.y, p.alpha * v.z, p.alpha * v.w};
+  if (p.beta != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) o[i] += p.beta * to_float(c[i]);
+  }
+  if (n >= 4 && p.vecC) {
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4 *>(c) = make_float4(o[0], o[1], o[2], o[3]);
+    else
+      *reinterpret_cast<uint2 *>(c) = make_uint2(pack2(o[0], o[1], T()), pack2(o[2], o[3], T()));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) from_float(c + i, o[i]);
+  }
+}
 // A thread's sums: ECOLS columns from c0 of row r, or (FRAG) its share of 32 rows from r.
 template <class Cfg, class T>
 __device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, int lane, const float (&acc)[Cfg::ECOLS]) {
@@ -457,57 +489,61 @@ __device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, i
     }
   }
 }
-// This CTA's share (rows rank * 128 / SPLIT ..) of a tile whose partial sums lie in the shared memory of
-// the cluster's CTAs: they are added in the CTAs' order, four columns at a time, with sixteen 16-byte
-// reads in flight per thread.
-template <class Cfg, class T, int SPLIT>
-__device__ __forceinline__ void fp8_reduce(const Fp8TcParams &p, uint32_t sbase, uint32_t rank, int r0, int c0) {
-  constexpr int ROWS = 128 / SPLIT, UNITS = ROWS * Cfg::BN / 4, THREADS = 32 * Cfg::EPI_WARPS;
-  constexpr int BATCH = SPLIT >= 8 ? 2 : 16 / SPLIT;
-  T *C = static_cast<T *>(p.C);
-  for (int u0 = threadIdx.x - 128; u0 < UNITS; u0 += THREADS * BATCH) {
-    float4 x[BATCH][SPLIT];
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      // consecutive threads: consecutive elements of a row of C
-      const int u = min(u0 + k * THREADS, UNITS - 1);
-      const int row = (Cfg::SWAP ? u % ROWS : u / (Cfg::BN / 4)) + ROWS * static_cast<int>(rank);
-      const int col = (Cfg::SWAP ? u / ROWS : u % (Cfg::BN / 4)) * 4;
-      const uint32_t at = sbase + 4 * (row * Cfg::PART_PITCH + col);
-#pragma unroll
-      for (int i = 0; i < SPLIT; ++i) x[k][i] = ld_dsmem_v4(map_to_rank(at, i));
-    }
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int u = u0 + k * THREADS;
-      if (u >= UNITS) break;
-      const int row = (Cfg::SWAP ? u % ROWS : u / (Cfg::BN / 4)) + ROWS * static_cast<int>(rank);
-      const int col = (Cfg::SWAP ? u / ROWS : u % (Cfg::BN / 4)) * 4;
-      float4 v = x[k][0];
-#pragma unroll
-      for (int i = 1; i < SPLIT; ++i) {
-        v.x += x[k][i].x;
-        v.y += x[k][i].y;
-        v.z += x[k][i].z;
-        v.w += x[k][i].w;
-      }
-      const int64_t r = r0 + row, c = c0 + col;
-      if (r >= p.rows) continue;
-      const float o[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (c + j < p.cols) fp8_put1(p, C + (Cfg::SWAP ? (c + j) * p.ldc + r : r * p.ldc + c + j), o[j]);
-    }
-  }
+// One of the cluster barrier's halves: threads that have read what they want from the other CTAs arrive
+// (nothing to release: their own writes are not for the cluster), and the last wait keeps every CTA's
+// shared memory alive until all have.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
-template <class Cfg, class T>
-__device__ __forceinline__ void fp8_reduce_tile(const Fp8TcParams &p, uint32_t sbase, uint32_t rank, int r0, int c0) {
-  if (p.split == 2)
-    fp8_reduce<Cfg, T, 2>(p, sbase, rank, r0, c0);
-  else if (p.split == 4)
-    fp8_reduce<Cfg, T, 4>(p, sbase, rank, r0, c0);
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// This CTA's share (rows rank * 128 / SPLIT ..) of a tile whose partial sums lie in the shared memory of
+// the cluster's CTAs: they are added in the CTAs' order, four elements of a row of C at a time.  All of a
+// thread's reads are in flight at once, and the CTA is done with its peers before it writes C.
+template <class Cfg, int SPLIT>
+__device__ __forceinline__ void fp8_reduce(const Fp8TcParams &p, uint32_t sbase, uint32_t rank, int r0, int c0) {
+  constexpr int ROWS = 128 / SPLIT, LINE = Cfg::SWAP ? ROWS : Cfg::BN;   // elements of a line that are this CTA's
+  constexpr int UNITS = ROWS * Cfg::BN / 4, THREADS = 32 * Cfg::EPI_WARPS, PER = (UNITS + THREADS - 1) / THREADS;
+  const int first = ROWS * static_cast<int>(rank);
+  const auto line_of = [&](int u) { return u / (LINE / 4) + (Cfg::SWAP ? 0 : first); };
+  const auto at_of = [&](int u) { return u % (LINE / 4) * 4 + (Cfg::SWAP ? first : 0); };
+  float4 x[PER][SPLIT];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int u = min(static_cast<int>(threadIdx.x) - 128 + k * THREADS, UNITS - 1);
+    const uint32_t at = sbase + 4 * (line_of(u) * Cfg::PART_PITCH + at_of(u));
+#pragma unroll
+    for (int i = 0; i < SPLIT; ++i) x[k][i] = ld_dsmem_v4(map_to_rank(at, i));
+  }
+#pragma unroll
+  for (int k = 0; k < PER; ++k)
+#pragma unroll
+    for (int i = 1; i < SPLIT; ++i) {
+      x[k][0].x += x[k][i].x;
+      x[k][0].y += x[k][i].y;
+      x[k][0].z += x[k][i].z;
+      x[k][0].w += x[k][i].w;
+    }
+  __syncwarp();
+  cluster_arrive_relaxed();
+  const int line0 = Cfg::SWAP ? c0 : r0, at0 = Cfg::SWAP ? r0 : c0;
+  const int lines = Cfg::SWAP ? p.cols : p.rows, length = Cfg::SWAP ? p.rows : p.cols;
+  const auto store = [&](auto type) {
+    using T = decltype(type);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int u = threadIdx.x - 128 + k * THREADS;
+      const int line = line0 + line_of(u), at = at0 + at_of(u);
+      if (u < UNITS && line < lines && at < length)
+        fp8_put4(p, static_cast<T *>(p.C) + line * p.ldc + at, x[k][0], length - at);
+    }
+  };
+  if (p.typeC == SGEMM_TYPE_F32)
+    store(float());
+  else if (p.typeC == SGEMM_TYPE_BF16)
+    store(__nv_bfloat16());
   else
-    fp8_reduce<Cfg, T, 8>(p, sbase, rank, r0, c0);
+    store(__half());
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -639,6 +675,9 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
           const int r = 32 * q + frag_row(j, lane), c = half * EC + frag_col(j, lane);
           *reinterpret_cast<float2 *>(smem + 4 * (r * Cfg::PART_PITCH + c)) = make_float2(acc[j], acc[j + 1]);
         }
+      } else if constexpr (Cfg::SWAP) {
+#pragma unroll
+        for (int j = 0; j < EC; ++j) reinterpret_cast<float *>(smem)[j * Cfg::PART_PITCH + row] = acc[j];
       } else {
 #pragma unroll
         for (int j = 0; j < EC; j += 4)
@@ -714,7 +753,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
       fp8_scales<Cfg>(p, sbase, bar, rank, lane);
     }
     __syncwarp();
-    if (shared_tile) cluster_sync();
+    if (shared_tile) {
+      cluster_sync();
+      cluster_arrive_relaxed();
+    }
   } else {
     if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_EPI));
     fp8_epilogue<Cfg>(p, smem, sbase, tmem, bar, rank, warp & 3, (warp >> 2) - 1, lane);
@@ -723,20 +765,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
       cluster_sync();   // every CTA's partial tile is written
       int r0, c0;
       fp8_tile<Cfg>(p, blockIdx.x / p.split, 0, r0, c0);
-      if (p.typeC == SGEMM_TYPE_F32)
-        fp8_reduce_tile<Cfg, float>(p, sbase, rank, r0, c0);
-      else if (p.typeC == SGEMM_TYPE_BF16)
-        fp8_reduce_tile<Cfg, __nv_bfloat16>(p, sbase, rank, r0, c0);
+      if (p.split == 2)
+        fp8_reduce<Cfg, 2>(p, sbase, rank, r0, c0);
+      else if (p.split == 4)
+        fp8_reduce<Cfg, 4>(p, sbase, rank, r0, c0);
       else
-        fp8_reduce_tile<Cfg, __half>(p, sbase, rank, r0, c0);
+        fp8_reduce<Cfg, 8>(p, sbase, rank, r0, c0);
       __syncwarp();
     }
   }
 
   tc_fence_before_sync();
   __syncthreads();
-  // the peers have read this CTA's partial tile; no CTA of a pair releases tensor memory early
-  if (Cfg::GROUP == 2 || shared_tile) cluster_sync();
+  if (Cfg::GROUP == 2) cluster_sync();   // no CTA of a pair releases tensor memory early
+  if (shared_tile) cluster_wait();
   if (warp == 1) {
     tc_fence_after_sync();
     if constexpr (Cfg::GROUP == 2)
