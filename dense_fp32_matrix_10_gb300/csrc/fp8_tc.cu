@@ -132,6 +132,7 @@ cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
 }
 
 using Pair = Fp8Tc<2, 256, false, false, 6, 1>;      // 256 x 256 on two SMs
+using PairStaged = Fp8Tc<2, 256, false, false, 5, 1, true>;   // the same for an unaligned C
 using PairVec = Fp8Tc<2, 256, false, true, 6, 1>;
 using Tile = Fp8Tc<1, 128, false, false, 3, 2>;      // 128 x 128, two CTAs an SM
 using TileVec = Fp8Tc<1, 128, false, true, 3, 2>;
@@ -148,16 +149,26 @@ bool tma_readable(const Fp8Operand &x, int64_t stored_rows) {
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Cycles that a product of `tiles` tiles of 128 x cols takes with `split` CTAs a tile, two CTAs an SM, as
-// measured: 920 for a block of k (the copies from the L2 cache bound either width), 4000 for a CTA's first
-// copies and its stores, and the exchange of partial tiles.
-int64_t tile_cycles(int64_t tiles, int64_t kblocks, int cols, int split, int64_t slots) {
-  return cdiv64(tiles * split, slots) * (cdiv64(kblocks, split) * 920 + 4000 + (split > 1 ? 1500 + 40 * cols : 0));
+// measured: 960 for a block of k (the copies from the L2 cache bound either width; 1150 with a scale per
+// column), 4000 for a CTA's first copies and its stores (more where C's rows are unaligned), and the exchange
+// of partial tiles.
+int64_t tile_cycles(int64_t tiles, int64_t kblocks, int cols, int split, int64_t slots, bool vec, bool aligned) {
+  const int64_t store = split > 1 ? 1500 + 40 * cols : aligned ? 0 : 40 * cols;
+  return cdiv64(tiles * split, slots) * (cdiv64(kblocks, split) * (vec ? 1150 : 960) + 4000 + store);
 }
-// CTAs per tile that make that least, each with two blocks or more.
-int pick_split(int64_t tiles, int64_t kblocks, int cols, int64_t slots) {
+// The same of the forms for few rows of C, which the weights' way from memory bounds: a block takes 700
+// cycles, or 560 a CTA where two share an SM.
+int64_t few_cycles(int64_t tiles, int64_t kblocks, int cols, int split, int64_t sms) {
+  const int64_t per_sm = cdiv64(tiles * split, sms);
+  return per_sm * (cdiv64(kblocks, split) * (per_sm > 1 ? 560 : 700) + 1500) +
+         (split > 1 ? 1500 + 20 * split * cols : 0);
+}
+// The split of at most `most` that makes `cycles(split)` least and leaves each CTA two blocks or more.
+template <class F>
+int pick_split(int64_t kblocks, int most, F cycles) {
   int best = 1;
-  for (int split = 2; split <= 8 && kblocks >= 2 * split; split *= 2)
-    if (tile_cycles(tiles, kblocks, cols, split, slots) < tile_cycles(tiles, kblocks, cols, best, slots)) best = split;
+  for (int split = 2; split <= most && kblocks >= 2 * split; split *= 2)
+    if (cycles(split) < cycles(best)) best = split;
   return best;
 }
 
@@ -170,18 +181,27 @@ bool fp8_tc_eligible(const Fp8Params &p) {
 cudaError_t launch_fp8_tc(const Fp8Params &p, int sm_count, cudaStream_t s) {
   const int64_t kb = cdiv64(p.K, 128), slots = 2 * sm_count;
   if (p.M <= 64 && !p.a.inner_rows) {
-    const int64_t tiles = cdiv64(p.N, 128);
-    if (p.M <= 16) return launch<Few16>(p, pick_split(tiles, kb, 16, slots), s);
-    if (p.M <= 32) return launch<Few32>(p, pick_split(tiles, kb, 32, slots), s);
-    return launch<Few64>(p, pick_split(tiles, kb, 64, slots), s);
+    const int cols = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
+    const int split =
+        pick_split(kb, 8, [&](int n) { return few_cycles(cdiv64(p.N, 128), kb, cols, n, sm_count); });
+    if (cols == 16) return launch<Few16>(p, split, s);
+    return cols == 32 ? launch<Few32>(p, split, s) : launch<Few64>(p, split, s);
   }
-  const bool vec = p.b.shift == 0;
-  const int64_t tiles = cdiv64(p.M, 128) * cdiv64(p.N, 128), halves = cdiv64(p.M, 128) * cdiv64(p.N, 64);
-  const int split = pick_split(tiles, kb, 128, slots), split_half = pick_split(halves, kb, 64, slots);
-  const int64_t tile = tile_cycles(tiles, kb, 128, split, slots), half = tile_cycles(halves, kb, 64, split_half, slots);
-  // a pair of SMs takes as long for a block of its 256 x 256 tile as two CTAs for one of theirs each
-  const int64_t pair = cdiv64(cdiv64(p.M, 256) * cdiv64(p.N, 256), sm_count / 2) * (kb * 920 + 3000);
-  if (pair <= tile && pair <= half) return vec ? launch<PairVec>(p, 1, s) : launch<Pair>(p, 1, s);
+  const bool vec = p.b.shift == 0, aligned = aligned_rows(p.C, p.ldc, p.typeC == SGEMM_TYPE_F32 ? 4 : 2, 16);
+  const int64_t rows = cdiv64(p.M, 128);
+  // (clusters of eight were never the best: 100 x 4096 x 4096 9.7 us with four, 16.0 with eight)
+  const auto tiles = [&](int n) { return tile_cycles(rows * cdiv64(p.N, 128), kb, 128, n, slots, vec, aligned); };
+  const auto halves = [&](int n) { return tile_cycles(rows * cdiv64(p.N, 64), kb, 64, n, slots, vec, aligned); };
+  const int split = pick_split(kb, 4, tiles), split_half = pick_split(kb, 4, halves);
+  const int64_t tile = tiles(split), half = halves(split_half);
+  // a pair of SMs takes as long for a block of its 256 x 256 tile as two CTAs for one of theirs each; its
+  // stores do not overlap another CTA's work
+  const int64_t pair =
+      1500 + cdiv64(cdiv64(p.M, 256) * cdiv64(p.N, 256), sm_count / 2) * (kb * 920 + (aligned ? 3000 : 8000));
+  if (pair <= tile && pair <= half) {
+    if (vec) return launch<PairVec>(p, 1, s);
+    return aligned ? launch<Pair>(p, 1, s) : launch<PairStaged>(p, 1, s);
+  }
   if (half < tile) return vec ? launch<HalfVec>(p, split_half, s) : launch<Half>(p, split_half, s);
   return vec ? launch<TileVec>(p, split, s) : launch<Tile>(p, split, s);
 }

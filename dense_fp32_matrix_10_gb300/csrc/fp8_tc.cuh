@@ -57,7 +57,8 @@ struct Fp8TcParams {
 
 // GROUP 2: a pair of CTAs computes 256 x BN (cta_group::2), each holding 128 rows and
 // half of the columns' operand.  SWAP: the tile's columns are C's rows.
-template <int GROUP_, int BN_, bool SWAP_, bool VEC_, int STAGES_, int CTAS_>
+// STAGED: see below.
+template <int GROUP_, int BN_, bool SWAP_, bool VEC_, int STAGES_, int CTAS_, bool STAGED_ = GROUP_ == 1>
 struct Fp8Tc {
   static constexpr int GROUP = GROUP_, BN = BN_, STAGES = STAGES_, CTAS = CTAS_;
   static constexpr bool SWAP = SWAP_, VEC = VEC_;
@@ -84,7 +85,16 @@ struct Fp8Tc {
   static constexpr int COL_SCALES = 128 * SCALE_BLOCKS;   // index of the first column scale
   static constexpr int SCALE_BYTES = 4 * (COL_SCALES + SCALE_BLOCKS * BN);
   static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
-  static constexpr int BAR_OFFSET = SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES;
+  // STAGED: rows of C may start off 16 bytes; a warp's finished 32 x 16 sums then pass through shared memory
+  // and are written two rows at a time (by a thread per row a C of 1000 x 1013 took 39 us, so 12; aligned rows
+  // are written faster by their threads, 16 bytes at a time).  Single CTAs use the stage ring for that.
+  // Pairs have a place for it only in the form for unaligned C: the 20 KB cost the aligned one 3 us of 74
+  // at 4096^3, as the L1 cache that holds the row scales shrinks.
+  static constexpr bool STAGED = STAGED_ && !SWAP && !FRAG;
+  static constexpr int STORE_PITCH = 20, STORE_BYTES = 32 * STORE_PITCH * 4;   // per warp
+  static constexpr int STORE_OFFSET = GROUP == 2 && STAGED ? SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES : 0;
+  static constexpr int BAR_OFFSET =
+      SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES + (GROUP == 2 && STAGED ? EPI_WARPS * STORE_BYTES : 0);
   static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 2 * SCALE_SLOTS + 1;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;
   static_assert(VEC || BN % 64 == 0, "a thread's columns lie in one block of 128");
@@ -462,9 +472,11 @@ __device__ __forceinline__ void fp8_put4(const Fp8TcParams &p, T *c, float4 v, i
       if (i < n) from_float(c + i, o[i]);
   }
 }
-// A thread's sums: ECOLS columns from c0 of row r, or (FRAG) its share of 32 rows from r.
+// The sums of a warp's 32 rows from r and ECOLS columns from c0: a thread holds those of row r + lane, or
+// (FRAG) pieces of four rows.  `stage`: the warp's STORE_BYTES of shared memory (STAGED).
 template <class Cfg, class T>
-__device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, int lane, const float (&acc)[Cfg::ECOLS]) {
+__device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, int lane, uint32_t stage,
+                                          const float (&acc)[Cfg::ECOLS]) {
   T *C = static_cast<T *>(p.C);
   if constexpr (Cfg::FRAG) {
 #pragma unroll
@@ -472,23 +484,51 @@ __device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, i
       const int row = r + frag_row(j, lane), col = c0 + frag_col(j, lane);
       if (row < p.rows && col < p.cols) fp8_put2(p, C + row * p.ldc + col, acc[j], acc[j + 1], col + 1 < p.cols);
     }
-  } else if (r >= p.rows) {
-    return;
   } else if constexpr (Cfg::SWAP) {
+    if (r + lane < p.rows) {
 #pragma unroll
-    for (int j = 0; j < Cfg::ECOLS; ++j)
-      if (c0 + j < p.cols) fp8_put1(p, C + (c0 + j) * p.ldc + r, acc[j]);
+      for (int j = 0; j < Cfg::ECOLS; ++j)
+        if (c0 + j < p.cols) fp8_put1(p, C + (c0 + j) * p.ldc + r + lane, acc[j]);
+    }
+  } else if (!Cfg::STAGED || p.vecC) {
+    if (r + lane < p.rows) {
+#pragma unroll
+      for (int j = 0; j < Cfg::ECOLS; j += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
+        const int n = p.cols - (c0 + j);
+        if (n > 0) fp8_put8(p, C + (r + lane) * p.ldc + c0 + j, v, n < 8 ? n : 8);
+      }
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < Cfg::ECOLS; j += 8) {
-      float v[8];
+    for (int j = 0; j < Cfg::ECOLS; j += 16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
-      const int n = p.cols - (c0 + j);
-      if (n > 0) fp8_put8(p, C + r * p.ldc + c0 + j, v, n < 8 ? n : 8);
+      for (int i = 0; i < 16; i += 4)
+        sts128(stage + 4 * (lane * Cfg::STORE_PITCH + i),
+               make_float4(acc[j + i], acc[j + i + 1], acc[j + i + 2], acc[j + i + 3]));
+      __syncwarp();
+      const int at = lane & 15, c = c0 + j + at;   // two rows at a time
+      if (c < p.cols) {
+#pragma unroll 1
+        for (int row = lane >> 4; row < 32; row += 16) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            asm volatile("ld.shared.f32 %0, [%1];"
+                         : "=f"(v[i])
+                         : "r"(stage + 4 * ((row + 2 * i) * Cfg::STORE_PITCH + at)));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (r + row + 2 * i < p.rows) fp8_put1(p, C + (r + row + 2 * i) * p.ldc + c, v[i]);
+        }
+      }
+      __syncwarp();
     }
   }
 }
+
 // One of the cluster barrier's halves: threads that have read what they want from the other CTAs arrive
 // (nothing to release: their own writes are not for the cluster), and the last wait keeps every CTA's
 // shared memory alive until all have.
@@ -685,13 +725,14 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
                  make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
       }
     } else {
-      const int c = c0 + half * EC, r = r0 + (Cfg::FRAG ? 32 * q : row);
+      const int c = c0 + half * EC, r = r0 + 32 * q;
+      const uint32_t stage = sbase + Cfg::STORE_OFFSET + (q + 4 * half) * Cfg::STORE_BYTES;
       if (p.typeC == SGEMM_TYPE_F32)
-        fp8_store<Cfg, float>(p, r, c, lane, acc);
+        fp8_store<Cfg, float>(p, r, c, lane, stage, acc);
       else if (p.typeC == SGEMM_TYPE_BF16)
-        fp8_store<Cfg, __nv_bfloat16>(p, r, c, lane, acc);
+        fp8_store<Cfg, __nv_bfloat16>(p, r, c, lane, stage, acc);
       else
-        fp8_store<Cfg, __half>(p, r, c, lane, acc);
+        fp8_store<Cfg, __half>(p, r, c, lane, stage, acc);
     }
   }
 }
