@@ -1,4 +1,6 @@
-"""Build the CUDA library in-tree: csrc/*.cu -> libsgemm_gb300.so (sm_103a only).
+"""Build the CUDA library in-tree: csrc/*.cu -> libsgemm_gb300.so (sm_103a only),
+and the extension module that marshals torch tensors for fp8.py
+(csrc/fp8_torch.cpp -> _fp8_torch.so, host code).
 
 Each translation unit is compiled by nvcc in parallel (one -gencode for
 compute capability 10.3a), objects go to ``_build/`` and are relinked only when
@@ -7,10 +9,12 @@ library depends on nothing but the driver at run time.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsgemm_gb300.so")
+TORCH_EXT = os.path.join(HERE, "_fp8_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xptxas", "-v",
@@ -47,6 +52,34 @@ def _compile(nvcc, src, obj, log, defines=()):
     return obj
 
 
+def _torch_extension(force: bool):
+    """Compile csrc/fp8_torch.cpp against the installed torch if it is out of date.  Without torch there is
+    nothing to marshal for."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    src, log = os.path.join(CSRC, "fp8_torch.cpp"), os.path.join(BUILD, "fp8_torch.log")
+    torch_dir = os.path.dirname(spec.origin)
+    newest = max([os.path.getmtime(src), os.path.getmtime(os.path.join(torch_dir, "version.py")),
+                  *(os.path.getmtime(h) for h in glob.glob(os.path.join(INCLUDE, "*.h")))])
+    if not force and os.path.exists(TORCH_EXT) and os.path.getmtime(TORCH_EXT) >= newest:
+        return TORCH_EXT
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    tmp = TORCH_EXT + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-I", INCLUDE, "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-isystem", cuda_include, src, "-o", tmp,
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    with open(log, "w") as f:
+        f.write(" ".join(cmd) + "\n" + proc.stdout + proc.stderr)
+    if proc.returncode != 0:
+        raise RuntimeError("g++ failed on fp8_torch.cpp:\n" + proc.stderr[-4000:])
+    os.replace(tmp, TORCH_EXT)
+    return TORCH_EXT
+
+
 def build(force: bool = False, jobs: int = None, verbose: bool = False, defines=(),
           out: str = None) -> str:
     """Compile and link if anything is out of date; return the library path.
@@ -71,10 +104,12 @@ def build(force: bool = False, jobs: int = None, verbose: bool = False, defines=
             os.path.getmtime(obj) < max(os.path.getmtime(src), newest_header)
         if stale:
             todo.append((src, obj, obj[:-2] + ".log"))
-    if todo:
-        jobs = jobs or min(len(todo), os.cpu_count() or 4)
-        with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-            list(ex.map(lambda t: _compile(nvcc, *t, defines=defines), todo))
+    jobs = jobs or min(len(todo) + 1, os.cpu_count() or 4)
+    with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        extension = None if out else ex.submit(_torch_extension, force)
+        list(ex.map(lambda t: _compile(nvcc, *t, defines=defines), todo))
+        if extension is not None:
+            extension.result()
     relink = force or bool(todo) or not os.path.exists(lib) or \
         os.path.getmtime(lib) < max(os.path.getmtime(o) for o in objs)
     if relink:

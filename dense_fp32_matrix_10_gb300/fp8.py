@@ -16,7 +16,10 @@ kernels read; any other layout gives the same results.
 All matrices are 2-D CUDA tensors with unit column stride and any row stride.
 Every function runs on ``stream`` (a torch.cuda.Stream; what it allocates then
 belongs to that stream) or on torch's current stream, and returns once its work
-is queued.  Nothing here computes; there is no CPU fallback.
+is queued.  Nothing here computes; there is no CPU fallback.  The usual calls
+(plain tensors of the current device, its current stream) are marshalled by the
+extension module _fp8_torch where it has been built; it hands back what it does
+not take, and the code here checks everything and says what is wrong.
 """
 import collections
 import ctypes
@@ -26,6 +29,7 @@ import torch
 from ._binding import SgemmError, _current_raw_stream, _op, load_library
 
 BLOCK = 128
+_BLOCKS = ((1, BLOCK), (BLOCK, 1), (BLOCK, BLOCK))
 TYPE_F32, TYPE_BF16, TYPE_F16, TYPE_E4M3, TYPE_E5M2 = 0, 1, 2, 8, 9
 _FLOAT = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
 _FP8 = {torch.float8_e4m3fn: TYPE_E4M3, torch.float8_e5m2: TYPE_E5M2}
@@ -38,6 +42,7 @@ RmsNormFp8.__doc__ = """What rms_norm_fp8 returns: the quantised norm and its sc
 (None without a residual), and, with training=True, the norm y in x's type and rstd."""
 
 _lib = None
+_usual = None   # the extension module, once the library is loaded
 _I64, _VP, _INT, _F = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 
 
@@ -59,6 +64,16 @@ def _library():
             f.restype = _INT
         lib.sgemm_rms_norm_backward_workspace.argtypes = [_I64, _I64]
         lib.sgemm_rms_norm_backward_workspace.restype = ctypes.c_size_t
+        global _usual
+        try:
+            from . import _fp8_torch
+        except ImportError:   # not built (or for another torch)
+            _usual = None
+        else:
+            _fp8_torch.bind(*(ctypes.cast(f, _VP).value for f in (
+                lib.sgemm_fp8, lib.sgemm_fp8_quantize, lib.sgemm_fp8_quantize_both, lib.sgemm_rms_norm_fp8,
+                lib.sgemm_rms_norm_backward, lib.sgemm_rms_norm_backward_workspace)))
+            _usual = _fp8_torch
         _lib = lib
     return _lib
 
@@ -182,10 +197,14 @@ def _fp8_type(dtype):
 def quantize_fp8(x, block=(1, BLOCK), dtype=torch.float8_e4m3fn, stream=None):
     """(q, scale) of a float32, bfloat16 or float16 matrix in blocks of (1, 128), (128, 1) or (128, 128):
     scale = max(max|x| / F, 2^-126) per block, q = x / scale rounded to `dtype`."""
+    if _usual is not None and stream is None and dtype in _FP8 and block in _BLOCKS:
+        r = _usual.quantize(x, *block, _FP8[dtype])
+        if r is not None:
+            return r
     px, rows, cols, ldx, tx, dev = _mat(x, "x", _FLOAT)
     tq = _fp8_type(dtype)
     br, bc = block
-    if (br, bc) not in ((1, BLOCK), (BLOCK, 1), (BLOCK, BLOCK)):
+    if (br, bc) not in _BLOCKS:
         raise ValueError("block must be (1, 128), (128, 1) or (128, 128)")
     ctx = _on(stream, dev)
     if ctx is not None:
@@ -203,6 +222,10 @@ def quantize_fp8(x, block=(1, BLOCK), dtype=torch.float8_e4m3fn, stream=None):
 
 def quantize_fp8_both(x, dtype=torch.float8_e4m3fn, stream=None):
     """(q_rows, scale_rows, q_cols, scale_cols): x in (1, 128) and in (128, 1) blocks, in one pass over it."""
+    if _usual is not None and stream is None and dtype in _FP8:
+        r = _usual.quantize_both(x, _FP8[dtype])
+        if r is not None:
+            return r
     px, rows, cols, ldx, tx, dev = _mat(x, "x", _FLOAT)
     tq = _fp8_type(dtype)
     ctx = _on(stream, dev)
@@ -244,6 +267,12 @@ def gemm_fp8(A, A_scale, B, B_scale, C=None, alpha=1.0, beta=0.0, transA=False, 
     128 elements along K and per 1 or 128 along M or N.  C is float32, bfloat16 or float16; if it is None a new
     M x N tensor of ``out_dtype`` (default bfloat16) is returned (beta must then be 0).
     """
+    if _usual is not None and stream is None:
+        tc = TYPE_BF16 if out_dtype is None else _FLOAT.get(out_dtype)
+        if tc is not None and (C is None or out_dtype is None or getattr(C, "dtype", None) == out_dtype):
+            r = _usual.product(A, A_scale, B, B_scale, C, alpha, beta, transA, transB, tc)
+            if r is not None:
+                return r
     pa, ra, ca, lda, fa, dev = _mat(A, "A", _FP8)
     pb, rb, cb, ldb, fb, devb = _mat(B, "B", _FP8)
     M, K = (ca, ra) if transA else (ra, ca)
@@ -288,6 +317,10 @@ def rms_norm_fp8(x, weight, residual=None, eps=1e-6, dtype=torch.float8_e4m3fn, 
     h = x + residual in x's type (None without a residual: h is x).  With training=True also y, the norm in x's
     type, and rstd = 1 / sqrt(mean(h^2) + eps) per row, which rms_norm_backward wants.  `weight` is float32 or of
     x's type."""
+    if _usual is not None and stream is None and dtype in _FP8:
+        r = _usual.norm(x, weight, residual, eps, _FP8[dtype], training)
+        if r is not None:
+            return RmsNormFp8._make(r)
     px, rows, cols, ldx, tx, dev = _mat(x, "x", _FLOAT)
     tq = _fp8_type(dtype)
     pw, tw, devw = _vec(weight, "weight", cols, _WEIGHT[tx])
@@ -325,6 +358,10 @@ def rms_norm_fp8(x, weight, residual=None, eps=1e-6, dtype=torch.float8_e4m3fn, 
 def rms_norm_backward(dy, h, weight, rstd, dh=None, stream=None):
     """(dx, dweight) of y = h * rstd * weight: dx (the gradient of x and of the residual alike, `dh` added to it)
     in h's type, dweight in weight's.  `dh` is the gradient that reaches h along the residual path."""
+    if _usual is not None and stream is None:
+        r = _usual.norm_backward(dy, h, weight, rstd, dh)
+        if r is not None:
+            return r
     pd, rows, cols, lddy, tx, dev = _mat(dy, "dy", _FLOAT)
     ph, hr, hc, ldh, _, devh = _mat(h, "h", _SAME[tx])
     if hr != rows or hc != cols:

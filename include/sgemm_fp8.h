@@ -108,7 +108,8 @@ SGEMM_API sgemm_status_t sgemm_fp8_quantize_both(int64_t rows, int64_t cols, con
  * X and R (NULL: h = x) are rows x cols of typeX (F32, BF16, F16), W has cols
  * elements of typeW (F32 or typeX).  Q and S are always written; H and Y (of
  * typeX) and T (rows floats) where not NULL.  Neither h nor y is rounded before
- * the later steps; H and Y hold them rounded to typeX.
+ * the later steps; H and Y hold them rounded to typeX.  rows == 0 or cols == 0
+ * do nothing (T is not written then either).
  */
 SGEMM_API sgemm_status_t sgemm_rms_norm_fp8(int64_t rows, int64_t cols, float eps, const void *X,
                                             int64_t ldx, const void *R, int64_t ldr,

@@ -561,6 +561,50 @@ def test_no_device_memory_of_the_librarys_own(sg):
         sg.sgemm_set_scratch_limit(old)
 
 
+# ---------------------------------------------------------------- the extension module
+def test_extension_is_built_and_bound(lib):
+    from dense_fp32_matrix_10_gb300 import fp8
+    assert fp8._usual is not None and fp8._usual.__file__.startswith(fp8.__file__.rsplit("/", 1)[0])
+
+
+def test_extension_leaves_the_unusual_to_python(lib):
+    from dense_fp32_matrix_10_gb300 import fp8
+    u, x = fp8._usual, torch.zeros(4, 8)
+    assert u.quantize(x, 1, 128, 8) is None and u.quantize_both(x, 8) is None        # not on a GPU
+    assert u.product(x, x, x, x, None, 1.0, 0.0, False, True, 1) is None
+    assert u.product(None, None, None, None, None, "1", 0.0, False, True, 1) is None
+    assert u.norm(x, x[0], None, 1e-6, 8, False) is None and u.norm_backward(x, x, x[0], x[0], None) is None
+    assert u.norm(x, x[0], None, 1e-6) is None                                       # arguments missing
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(1, 128), (5, 0), (0, 7), (70, 333), (257, 1024)])
+def test_both_ways_through_python(sg, monkeypatch, shape):
+    """The extension module and the general code hand over the same calls."""
+    from dense_fp32_matrix_10_gb300 import fp8
+    rows, cols = shape
+    x, r = (torch.randn(shape, generator=rng(140 + i), device="cuda").bfloat16() for i in range(2))
+    w = torch.randn(cols, generator=rng(142), device="cuda")
+    qb, sb, _ = operand(96, cols, B, E4M3, False, 143)
+    c = torch.randn(rows, 100, generator=rng(144), device="cuda")[:, :96]
+
+    def everything():
+        o = sg.rms_norm_fp8(x, w, residual=r, training=True)
+        q, s = sg.quantize_fp8(x)
+        out = [*o[:5 if cols else 4], q, s]   # (rows of no elements have no rstd)
+        out += [*sg.quantize_fp8(x, (B, 1), E5M2), *sg.quantize_fp8_both(x)]
+        out += [*sg.rms_norm_backward(x, o.h, w, o.rstd, dh=r), *sg.rms_norm_backward(x, o.h, w, o.rstd)]
+        for kw in (dict(), dict(out_dtype=torch.float32, alpha=0.5), dict(C=c.clone(), beta=1.0)):
+            out.append(sg.gemm_fp8(q, s, qb, sb, transB=True, **kw))
+        return out
+
+    ours = everything()
+    monkeypatch.setattr(fp8, "_usual", None)
+    for a, b in zip(ours, everything()):
+        assert a.dtype == b.dtype and a.shape == b.shape and a.stride() == b.stride()
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
 # ---------------------------------------------------------------- refusals
 @pytest.fixture(scope="module")
 def lib(sg):
