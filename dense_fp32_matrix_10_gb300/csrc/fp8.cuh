@@ -51,17 +51,6 @@ __device__ __forceinline__ uint2 to_fp8x8(const float (&v)[8], float mul, bool e
   }
   return u;
 }
-// Two 8-bit elements -> two floats (exact: both types are subsets of F16).
-__device__ __forceinline__ float2 from_fp8x2(uint32_t u, bool e5m2) {
-  uint32_t h;
-  const uint16_t b = static_cast<uint16_t>(u);
-  if (e5m2)
-    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(b));
-  else
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(b));
-  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
-
 // ------------------------------------------------------------ F32, BF16, F16
 // Raw<T>: eight consecutive elements as loaded.
 template <class T> struct Raw;

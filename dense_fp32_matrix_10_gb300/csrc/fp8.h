@@ -32,12 +32,9 @@ struct Fp8Params {
   int *status;
 };
 
-// CUDA cores, any layout (fp8_simt.cu).
-cudaError_t launch_fp8_simt(const Fp8Params &p, cudaStream_t s);
-// Tensor cores, operands that TMA can read: 16-byte aligned rows (fp8_tc.cu).
-bool fp8_tc_eligible(const Fp8Params &p);
-cudaError_t launch_fp8_tc(const Fp8Params &p, int sm_count, cudaStream_t s);
-// C = beta * C (fp8_simt.cu).
+// The product on the tensor cores, any layout (fp8_tc.cu).
+cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s);
+// C = beta * C (fp8_scale_c.cu).
 cudaError_t launch_fp8_scale_c(const Fp8Params &p, cudaStream_t s);
 
 struct QuantizeParams {

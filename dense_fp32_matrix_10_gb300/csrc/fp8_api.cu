@@ -122,7 +122,7 @@ sgemm_status_t sgemm_fp8(int transA, int transB, int64_t M, int64_t N, int64_t K
   p.status = d->status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!product) return queued(launch_fp8_scale_c(p, s), 1);
-  return queued(fp8_tc_eligible(p) ? launch_fp8_tc(p, d->sm_count, s) : launch_fp8_simt(p, s), 1);
+  return queued(launch_fp8_product(p, d->sm_count, s), 1);
 }
 
 sgemm_status_t sgemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, sgemm_type_t typeX, int64_t ldx, void *Q,

@@ -31,7 +31,7 @@ __device__ __forceinline__ float max_of_8x16(const float (&v)[8], int lane16) {
 }
 
 template <class T, int MODE>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 && MODE != (kRow | kCol) ? 3 : 2)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
     quantize_kernel(const QuantizeParams p, const int64_t tiles_c, const bool vec_x, const bool vec_r,
                     const bool vec_c) {
   __shared__ float part[8][128];   // column maxima of each warp, then of the tile
@@ -130,6 +130,98 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && MODE != (kRow | kCol) ?
   }
 }
 
+// Both quantisations of 16-bit elements.  In registers (as above) the tile, its maxima and their use took 117
+// registers and two CTAs an SM, too few bytes in flight (16384 x 8192 116 us, 4.6 TB/s); here the tile lies in
+// shared memory, put there by asynchronous copies, and five CTAs fit (XXX us).  Of F32, whose tile takes
+// twice the room, the registers are as fast (4096 x 8192 38 against 42 us).
+template <class T>
+__global__ void __launch_bounds__(256, 5)
+    quantize_both_kernel(const QuantizeParams p, const int64_t tiles_c, const bool vec_x, const bool vec_r,
+                         const bool vec_c) {
+  constexpr int PITCH = 128 + 16 / sizeof(T);   // a 16-byte unit more: rows start in different banks
+  extern __shared__ __align__(16) unsigned char tile_smem[];
+  T *tile = reinterpret_cast<T *>(tile_smem);
+  __shared__ __align__(16) float part[8][128];   // column maxima of 16 rows, then (part[0]) 1 / scale
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+  const int lane16 = threadIdx.x & 15, row16 = threadIdx.x >> 4;
+  const int64_t c0 = tc * 128 + lane16 * 8, r0 = tr * 128 + row16;   // this thread's rows: r0 + 16 i
+  const int64_t left = p.cols - c0;
+  const int n = left < 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
+  const int rows = static_cast<int>(min(int64_t(128), p.rows - r0));
+  T *mine = tile + row16 * PITCH + lane16 * 8;
+  {
+    const T *x = static_cast<const T *>(p.x) + r0 * p.ldx + c0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = 16 * i < rows ? n : 0;
+      if (k == 8 && vec_x) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(mine + 16 * i * PITCH)),
+                     "l"(x + 16 * i * p.ldx)
+                     : "memory");
+      } else {
+        float v[8];
+        unpack(load8(x + 16 * i * p.ldx, k, false), v);
+        store8(mine + 16 * i * PITCH, v, 8, true);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  __syncthreads();
+  // maxima of 16 rows by 4 columns
+  {
+    const int c = (threadIdx.x & 31) * 4, r = (threadIdx.x >> 5) * 16;
+    float m[4] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const T *x = tile + (r + i) * PITCH + c;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = max_abs(m[j], to_float(x[j]));
+    }
+    *reinterpret_cast<float4 *>(&part[threadIdx.x >> 5][c]) = make_float4(m[0], m[1], m[2], m[3]);
+  }
+  float rmax[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    unpack(load8(mine + 16 * i * PITCH, 8, true), v);
+    rmax[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rmax[i] = max_abs(rmax[i], v[j]);
+  }
+  const int own = owned(lane16);
+  const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), row_inv = __fdiv_rn(1.0f, s);
+  if ((lane16 & 1) == 0 && 16 * own < rows) p.sr[(r0 + 16 * own) * p.ldsr + tc] = s;
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    float a = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) a = max_abs(a, part[w][threadIdx.x]);
+    const float t = block_scale(a, p.e5m2);
+    const int64_t c = tc * 128 + threadIdx.x;
+    if (c < p.cols) p.sc[tr * p.ldsc + c] = t;
+    part[0][threadIdx.x] = __fdiv_rn(1.0f, t);
+  }
+  __syncthreads();
+  float inv[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) inv[j] = part[0][lane16 * 8 + j];
+  unsigned char *qr = p.qr + r0 * p.ldqr + c0, *qc = p.qc + r0 * p.ldqc + c0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float f = __shfl_sync(~0u, row_inv, (i & 4) * 2 + (i & 2) * 2 + (i & 1) * 2, 16);
+    float v[8];
+    unpack(load8(mine + 16 * i * PITCH, 8, true), v);
+    if (16 * i < rows) {
+      store8_fp8(qr + 16 * i * p.ldqr, to_fp8x8(v, f, p.e5m2), n, vec_r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= inv[j];
+      store8_fp8(qc + 16 * i * p.ldqc, to_fp8x8(v, 1.0f, p.e5m2), n, vec_c);
+    }
+  }
+}
+
 template <class T>
 cudaError_t launch_typed(const QuantizeParams &p, cudaStream_t s) {
   const int64_t tiles_c = (p.cols + 127) / 128, tiles = tiles_c * ((p.rows + 127) / 128);
@@ -139,7 +231,14 @@ cudaError_t launch_typed(const QuantizeParams &p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(tiles)), block(256);
   auto go = [&](auto kernel) { return launch_maybe_pdl(kernel, grid, block, 0, s, true, p, tiles_c, vx, vr, vc); };
   if (p.tile) return go(quantize_kernel<T, kTile>);
-  if (p.qr && p.qc) return go(quantize_kernel<T, kRow | kCol>);
+  if (p.qr && p.qc) {
+    if constexpr (sizeof(T) == 4) {
+      return go(quantize_kernel<T, kRow | kCol>);
+    } else {
+      constexpr int smem = 128 * (128 * static_cast<int>(sizeof(T)) + 16);
+      return launch_maybe_pdl(quantize_both_kernel<T>, grid, block, smem, s, true, p, tiles_c, vx, vr, vc);
+    }
+  }
   return p.qr ? go(quantize_kernel<T, kRow>) : go(quantize_kernel<T, kCol>);
 }
 

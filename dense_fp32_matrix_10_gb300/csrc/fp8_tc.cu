@@ -91,11 +91,16 @@ cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
   Fp8TcParams t;
   t.rows = Cfg::SWAP ? p.N : p.M;
   t.cols = Cfg::SWAP ? p.M : p.N;
-  CUtensorMap tm_row, tm_col;
+  t.row_q = row.q;
+  t.col_q = col.q;
+  t.row_qld = row.ld;
+  t.col_qld = col.ld;
+  t.k = p.K;
+  CUtensorMap tm_row = {}, tm_col = {};
   const auto encode = [&](CUtensorMap *m, const Fp8Operand &x, int outer, int box) {
     return x.inner_rows ? encode_u8(m, x, p.K, outer, 128) : encode_u8(m, x, outer, p.K, box);
   };
-  if (!encode(&tm_row, row, t.rows, 128) || !encode(&tm_col, col, t.cols, Cfg::BN / Cfg::GROUP))
+  if (!Cfg::LOAD && (!encode(&tm_row, row, t.rows, 128) || !encode(&tm_col, col, t.cols, Cfg::BN / Cfg::GROUP)))
     return cudaErrorInvalidValue;
   t.row_s = row.s;
   t.col_s = col.s;
@@ -142,8 +147,12 @@ using Few16 = Fp8Tc<1, 16, true, true, 5, 2>;        // up to 16, 32, 64 rows of
 using Few32 = Fp8Tc<1, 32, true, true, 5, 2>;        // tile's rows)
 using Few64 = Fp8Tc<1, 64, true, true, 4, 2>;
 
+using Loaded = Fp8Tc<1, 128, false, false, 5, 1, true, true>;   // 128 x 128 of operands that TMA cannot read
+using LoadedVec = Fp8Tc<1, 128, false, true, 5, 1, true, true>;
+
+// 16-byte aligned rows that a tensor map can describe.
 bool tma_readable(const Fp8Operand &x, int64_t stored_rows) {
-  return reinterpret_cast<uintptr_t>(x.q) % 16 == 0 && (x.ld % 16 == 0 || stored_rows == 1);
+  return reinterpret_cast<uintptr_t>(x.q) % 16 == 0 && (stored_rows == 1 || (x.ld % 16 == 0 && x.ld < kMaxLd));
 }
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -174,13 +183,11 @@ int pick_split(int64_t kblocks, int most, F cycles) {
 
 }  // namespace
 
-bool fp8_tc_eligible(const Fp8Params &p) {
-  return tma_readable(p.a, p.a.inner_rows ? p.K : p.M) && tma_readable(p.b, p.b.inner_rows ? p.K : p.N);
-}
-
-cudaError_t launch_fp8_tc(const Fp8Params &p, int sm_count, cudaStream_t s) {
+cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s) {
   const int64_t kb = cdiv64(p.K, 128), slots = 2 * sm_count;
-  if (p.M <= 64 && !p.a.inner_rows) {
+  const bool readable =
+      tma_readable(p.a, p.a.inner_rows ? p.K : p.M) && tma_readable(p.b, p.b.inner_rows ? p.K : p.N);
+  if (p.M <= 64 && !p.a.inner_rows && readable) {
     const int cols = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
     const int split =
         pick_split(kb, 8, [&](int n) { return few_cycles(cdiv64(p.N, 128), kb, cols, n, sm_count); });
@@ -192,6 +199,12 @@ cudaError_t launch_fp8_tc(const Fp8Params &p, int sm_count, cudaStream_t s) {
   // (clusters of eight were never the best: 100 x 4096 x 4096 9.7 us with four, 16.0 with eight)
   const auto tiles = [&](int n) { return tile_cycles(rows * cdiv64(p.N, 128), kb, 128, n, slots, vec, aligned); };
   const auto halves = [&](int n) { return tile_cycles(rows * cdiv64(p.N, 64), kb, 64, n, slots, vec, aligned); };
+  if (!readable) {   // one CTA an SM, and 2500 cycles a block
+    const int n = pick_split(kb, 4, [&](int n) {
+      return tile_cycles(rows * cdiv64(p.N, 128), 3 * kb, 128, n, sm_count, false, aligned);
+    });
+    return vec ? launch<LoadedVec>(p, n, s) : launch<Loaded>(p, n, s);
+  }
   const int split = pick_split(kb, 4, tiles), split_half = pick_split(kb, 4, halves);
   const int64_t tile = tiles(split), half = halves(split_half);
   // a pair of SMs takes as long for a block of its 256 x 256 tile as two CTAs for one of theirs each; its

@@ -22,6 +22,7 @@
 //            (cp.async: any stride, zeros past the edge)
 //   warp 3   idle
 //   warps 4+ epilogue; warp 4 + q + 4 h owns rows 32 q .. +31 and the h-th ECOLS columns
+//   LOAD: four more warps in the place of the producer
 // Every wait on an mbarrier is bounded; after giving up, a role lets its copies and
 // MMAs land (bounded) and goes to the barriers at the end.
 #pragma once
@@ -38,6 +39,9 @@
 namespace sg {
 
 struct Fp8TcParams {
+  const unsigned char *row_q, *col_q;   // operands as stored and their row strides (LOAD)
+  int64_t row_qld, col_qld;
+  int k;
   const float *row_s, *col_s;         // scales
   int64_t row_ld, col_ld;             // their row strides
   int row_shift, col_shift;           // outer index >> shift = scale index
@@ -57,11 +61,13 @@ struct Fp8TcParams {
 
 // GROUP 2: a pair of CTAs computes 256 x BN (cta_group::2), each holding 128 rows and
 // half of the columns' operand.  SWAP: the tile's columns are C's rows.
-// STAGED: see below.
-template <int GROUP_, int BN_, bool SWAP_, bool VEC_, int STAGES_, int CTAS_, bool STAGED_ = GROUP_ == 1>
+// STAGED: see below.  LOAD: four more warps read operands that TMA cannot, of any base and stride.
+template <int GROUP_, int BN_, bool SWAP_, bool VEC_, int STAGES_, int CTAS_, bool STAGED_ = GROUP_ == 1,
+          bool LOAD_ = false>
 struct Fp8Tc {
   static constexpr int GROUP = GROUP_, BN = BN_, STAGES = STAGES_, CTAS = CTAS_;
-  static constexpr bool SWAP = SWAP_, VEC = VEC_;
+  static constexpr bool SWAP = SWAP_, VEC = VEC_, LOAD = LOAD_;
+  static_assert(!LOAD || (GROUP == 1 && BN == 128), "loaded operands: 128 x 128 tiles of one CTA");
   // (a tile of 64 columns takes the room of 128: of an outer-contiguous operand whole 128-byte rows are
   // copied, and it uses one half of them)
   static constexpr bool HALF_ROWS = BN == 64 && !SWAP_;
@@ -71,12 +77,12 @@ struct Fp8Tc {
   static constexpr int TMEM_COLS = ACCS * BN;
   static constexpr int ECOLS = BN == 256 ? 128 : BN;   // columns a thread adds up
   static constexpr int EPI_WARPS = 4 * (BN / ECOLS);
-  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS + (LOAD ? 128 : 0);
   // FRAG: a thread holds 4 rows and every fourth pair of columns instead of one row, so it reads a
   // quarter of the column scales.  A shared memory read fills 128 bytes of registers a cycle however
   // many lanes share an address: 128 scales for each of 256 threads and block are 1024 cycles, more
   // than the block's MMAs take (4096 x 4096 x 16384: 448 us with one row a thread, XXX so).
-  static constexpr bool FRAG = VEC && !SWAP && ECOLS == 128;
+  static constexpr bool FRAG = VEC && !SWAP && BN >= 128;
   static constexpr int CHUNK = ECOLS == 128 ? 32 : ECOLS == 64 ? 16 : ECOLS / 2;   // columns of a tensor memory load
   static_assert(ECOLS / CHUNK % 2 == 0, "chunks alternate between two buffers across blocks");
   // VEC: ring of scales, SCALE_BLOCKS blocks of k a slot (one wait per slot, not per block): the rows'
@@ -103,7 +109,8 @@ struct Fp8Tc {
   // ECOLS = 128: 128 sums and two chunks of 32 in flight per epilogue thread
   static constexpr bool SPLIT_REGS = ECOLS == 128;
   static constexpr int REGS_WG0 = 40, REGS_EPI = BN == 256 ? 232 : 216;
-  static constexpr int SPLIT_TOTAL = 128 * REGS_WG0 + 32 * EPI_WARPS * REGS_EPI;
+  static constexpr int SPLIT_TOTAL =
+      128 * REGS_WG0 + 32 * EPI_WARPS * REGS_EPI + (LOAD ? 128 * ((65536 / CTAS / THREADS) & ~7) : 0);
   static_assert(!SPLIT_REGS || SPLIT_TOTAL <= THREADS * ((65536 / CTAS / THREADS) & ~7),
                 "register split exceeds the launch budget");
   // a cluster's partial tiles, in the stage ring: lines along C's rows ([row][column], SWAP [column][row]),
@@ -212,8 +219,9 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t cbar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
 
-// FRAG: 32 rows x 32 columns in pieces of 8 x 2 per four lanes: lane l gets rows l / 4 + 8 i and
-// columns 8 n + 2 (l % 4) + {0, 1} in v[16 (i / 2) + 4 n + 2 (i % 2) + {0, 1}].
+// FRAG: 32 rows x 32 or 16 columns in pieces of 8 x 2 per four lanes.  With H registers for either half of
+// the 32 TMEM lanes, lane l gets rows l / 4 + 8 i and columns 8 n + 2 (l % 4) + {0, 1} in
+// v[H (i / 2) + 4 n + 2 (i % 2) + {0, 1}].
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&v)[32]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {   // lanes 0..15, 16..31
@@ -224,6 +232,15 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&v)[32]) 
         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
           "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
         : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16)));
+  }
+}
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t *o = v + 8 * h;
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7])
+                 : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16)));
   }
 }
 template <class Cfg>
@@ -302,6 +319,69 @@ __device__ __forceinline__ void fp8_produce(const Fp8TcParams &p, const CUtensor
   if (!ok && rank == 0) {   // the copies in flight land before the CTA may end
     for (uint32_t j = it > Cfg::STAGES ? it - Cfg::STAGES : 0; j < it; ++j)
       wait_parity_bounded(bar.full(j % Cfg::STAGES), (j / Cfg::STAGES) & 1, p.wait_budget_ns, nullptr);
+  }
+}
+
+// ------------------------------------------------------------------ loaders
+// 16 bytes from x of row y of a stored matrix, zeros outside.  Where the aligned words around them lie within
+// the matrix (its rows and what is between them), five words and a shift; else byte by byte.
+__device__ __forceinline__ uint4 load16(const unsigned char *q, int64_t ld, int rows, int cols, int y, int x) {
+  uint32_t w[4] = {0, 0, 0, 0};
+  if (y < rows && x < cols) {
+    const unsigned char *p = q + y * ld + x;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p), low = at & ~uintptr_t(3);
+    const unsigned char *end = q + (rows - 1) * ld + cols;
+    if (x + 16 <= cols && low >= reinterpret_cast<uintptr_t>(q) && low + 20 <= reinterpret_cast<uintptr_t>(end)) {
+      const uint32_t *s = reinterpret_cast<const uint32_t *>(low);
+      const uint32_t shift = 8 * static_cast<uint32_t>(at & 3);
+      uint32_t v[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) v[i] = s[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], shift);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (x + i < cols) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// One box of 128 rows of 128 bytes at (y0, x0) by 128 threads, in the layout a 128-byte-swizzled TMA box has.
+__device__ __forceinline__ void load_box(uint32_t dst, const unsigned char *q, int64_t ld, int rows, int cols, int y0,
+                                         int x0, int thread) {
+#pragma unroll 2
+  for (int i = 0; i < 8; ++i) {   // eight threads a row, sixteen rows at a time
+    const int r = 16 * i + thread / 8, c = thread % 8;
+    const uint4 v = load16(q, ld, rows, cols, y0 + r, x0 + 16 * c);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 128 * r + 16 * (c ^ (r & 7))), "r"(v.x),
+                 "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+  }
+}
+template <class Cfg>
+__device__ __forceinline__ void fp8_load(const Fp8TcParams &p, uint32_t sbase, const Fp8Bars<Cfg> &bar, int thread) {
+  const Fp8Work<Cfg> w(p);
+  uint32_t it = 0;
+  for (int t = w.first; t < p.num_tiles; t += w.step) {
+    int r0, c0;
+    fp8_tile<Cfg>(p, t, 0, r0, c0);
+    for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+      const uint32_t s = it % Cfg::STAGES, round = it / Cfg::STAGES;
+      if (round > 0 && !wait_parity_bounded(bar.empty(s), (round - 1) & 1, p.wait_budget_ns, p.status)) return;
+      const uint32_t st = sbase + s * Cfg::STAGE_BYTES;
+      const int k0 = kb * 128;
+      if (p.row_inner)
+        load_box(st, p.row_q, p.row_qld, p.k, p.rows, k0, r0, thread);
+      else
+        load_box(st, p.row_q, p.row_qld, p.rows, p.k, r0, k0, thread);
+      if (p.col_inner)
+        load_box(st + Cfg::ROW_BYTES, p.col_q, p.col_qld, p.k, p.cols, k0, c0, thread);
+      else
+        load_box(st + Cfg::ROW_BYTES, p.col_q, p.col_qld, p.cols, p.k, c0, k0, thread);
+      fence_proxy_async_smem();   // the tensor cores read through the async proxy
+      mbar_arrive(bar.full(s));
+    }
   }
 }
 
@@ -429,9 +509,15 @@ __device__ __forceinline__ void fp8_put1(const Fp8TcParams &p, T *c, float v) {
   if (p.beta != 0.0f) v += p.beta * to_float(*c);
   from_float(c, v);
 }
-// FRAG: row and column, in the warp's 32 x 128, of a thread's sums j and j + 1 (j even; chunks of 32).
-__device__ __forceinline__ int frag_row(int j, int lane) { return lane / 4 + 16 * (j % 32 / 16) + 8 * (j / 2 % 2); }
-__device__ __forceinline__ int frag_col(int j, int lane) { return j / 32 * 32 + j % 16 / 4 * 8 + 2 * (lane & 3); }
+// FRAG: row and column, in the warp's 32 x ECOLS, of a thread's sums j and j + 1 (j even).
+template <class Cfg>
+__device__ __forceinline__ int frag_row(int j, int lane) {
+  return lane / 4 + 16 * (j % Cfg::CHUNK / (Cfg::CHUNK / 2)) + 8 * (j / 2 % 2);
+}
+template <class Cfg>
+__device__ __forceinline__ int frag_col(int j, int lane) {
+  return j / Cfg::CHUNK * Cfg::CHUNK + j % (Cfg::CHUNK / 2) / 4 * 8 + 2 * (lane & 3);
+}
 
 // Two consecutive elements of a row of C at an even column, the second if `two`.
 template <class T>
@@ -481,7 +567,7 @@ __device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, i
   if constexpr (Cfg::FRAG) {
 #pragma unroll
     for (int j = 0; j < Cfg::ECOLS; j += 2) {
-      const int row = r + frag_row(j, lane), col = c0 + frag_col(j, lane);
+      const int row = r + frag_row<Cfg>(j, lane), col = c0 + frag_col<Cfg>(j, lane);
       if (row < p.rows && col < p.cols) fp8_put2(p, C + row * p.ldc + col, acc[j], acc[j + 1], col + 1 < p.cols);
     }
   } else if constexpr (Cfg::SWAP) {
@@ -661,7 +747,7 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
         float2 f[CH / 2];
         if constexpr (Cfg::FRAG) {
 #pragma unroll
-          for (int n = 0; n < 4; ++n) f[n] = *reinterpret_cast<const float2 *>(sc + cc * CH + 8 * n + 2 * (lane & 3));
+          for (int n = 0; n < CH / 8; ++n) f[n] = *reinterpret_cast<const float2 *>(sc + cc * CH + 8 * n + 2 * (lane & 3));
         } else if constexpr (Cfg::VEC) {
 #pragma unroll
           for (int j = 0; j < CH; j += 4) {
@@ -691,7 +777,7 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
         for (int j = 0; j < CH; j += 2) {
           float *o = acc + cc * CH + j;
           const float2 a = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-          const float2 c = Cfg::FRAG  ? __fmul2_rn(f[j % 16 / 4], rs[j / 16 * 2 + j / 2 % 2])
+          const float2 c = Cfg::FRAG  ? __fmul2_rn(f[j % (CH / 2) / 4], rs[j / (CH / 2) * 2 + j / 2 % 2])
                            : Cfg::VEC ? f[j / 2]
                                       : rs[0];
           const float2 sum = __ffma2_rn(a, c, make_float2(o[0], o[1]));
@@ -712,7 +798,7 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
       if constexpr (Cfg::FRAG) {
 #pragma unroll
         for (int j = 0; j < EC; j += 2) {
-          const int r = 32 * q + frag_row(j, lane), c = half * EC + frag_col(j, lane);
+          const int r = 32 * q + frag_row<Cfg>(j, lane), c = half * EC + frag_col<Cfg>(j, lane);
           *reinterpret_cast<float2 *>(smem + 4 * (r * Cfg::PART_PITCH + c)) = make_float2(acc[j], acc[j + 1]);
         }
       } else if constexpr (Cfg::SWAP) {
@@ -754,7 +840,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
-      mbar_init(bar.full(s), 1);
+      mbar_init(bar.full(s), Cfg::LOAD ? 128 : 1);
       mbar_init(bar.empty(s), 1);
     }
     for (int b = 0; b < Cfg::ACCS; ++b) {
@@ -767,8 +853,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
     mbar_init(bar.drain(), 1);
     fence_mbar_init();
-    tma_prefetch_desc(&tm_row);
-    tma_prefetch_desc(&tm_col);
+    if (!Cfg::LOAD) {
+      tma_prefetch_desc(&tm_row);
+      tma_prefetch_desc(&tm_col);
+    }
   }
   if (warp == 1) {
     if constexpr (Cfg::GROUP == 2)
@@ -787,12 +875,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
   if (warp < 4) {
     if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_WG0));
     if (warp == 0) {
-      if (lane == 0) fp8_produce<Cfg>(p, &tm_row, &tm_col, sbase, bar, Cfg::GROUP == 2 ? rank : 0);
+      if (!Cfg::LOAD && lane == 0) fp8_produce<Cfg>(p, &tm_row, &tm_col, sbase, bar, Cfg::GROUP == 2 ? rank : 0);
     } else if (warp == 1) {
       if (lane == 0 && (Cfg::GROUP == 1 || rank == 0)) fp8_issue<Cfg>(p, sbase, tmem, bar);
     } else if (Cfg::VEC && warp == 2) {
       fp8_scales<Cfg>(p, sbase, bar, rank, lane);
     }
+    __syncwarp();
+    if (shared_tile) {
+      cluster_sync();
+      cluster_arrive_relaxed();
+    }
+  } else if (Cfg::LOAD && warp >= 4 + Cfg::EPI_WARPS) {
+    fp8_load<Cfg>(p, sbase, bar, threadIdx.x - 128 - 32 * Cfg::EPI_WARPS);
     __syncwarp();
     if (shared_tile) {
       cluster_sync();
