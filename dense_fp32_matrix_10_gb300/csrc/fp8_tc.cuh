@@ -323,40 +323,53 @@ __device__ __forceinline__ void fp8_produce(const Fp8TcParams &p, const CUtensor
 }
 
 // ------------------------------------------------------------------ loaders
-// 16 bytes from x of row y of a stored matrix, zeros outside.  Where the aligned words around them lie within
-// the matrix (its rows and what is between them), five words and a shift; else byte by byte.
+// 16 bytes from x of row y of a stored matrix, one by one, zeros outside.
 __device__ __forceinline__ uint4 load16(const unsigned char *q, int64_t ld, int rows, int cols, int y, int x) {
   uint32_t w[4] = {0, 0, 0, 0};
-  if (y < rows && x < cols) {
+  if (y < rows) {
     const unsigned char *p = q + y * ld + x;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p), low = at & ~uintptr_t(3);
-    const unsigned char *end = q + (rows - 1) * ld + cols;
-    if (x + 16 <= cols && low >= reinterpret_cast<uintptr_t>(q) && low + 20 <= reinterpret_cast<uintptr_t>(end)) {
-      const uint32_t *s = reinterpret_cast<const uint32_t *>(low);
-      const uint32_t shift = 8 * static_cast<uint32_t>(at & 3);
-      uint32_t v[5];
 #pragma unroll
-      for (int i = 0; i < 5; ++i) v[i] = s[i];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], shift);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (x + i < cols) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
-    }
+    for (int i = 0; i < 16; ++i)
+      if (x + i < cols) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// One box of 128 rows of 128 bytes at (y0, x0) by 128 threads, in the layout a 128-byte-swizzled TMA box has.
+// One box of 128 rows of 128 bytes at (y0, x0) by 128 threads, in the layout a 128-byte-swizzled TMA box has:
+// eight threads a row, sixteen rows at a time.  A thread whose first and last pieces can be read by words reads
+// all eight so, twenty loads in flight.
 __device__ __forceinline__ void load_box(uint32_t dst, const unsigned char *q, int64_t ld, int rows, int cols, int y0,
                                          int x0, int thread) {
-#pragma unroll 2
-  for (int i = 0; i < 8; ++i) {   // eight threads a row, sixteen rows at a time
-    const int r = 16 * i + thread / 8, c = thread % 8;
-    const uint4 v = load16(q, ld, rows, cols, y0 + r, x0 + 16 * c);
+  const int c = thread % 8, r0 = thread / 8, x = x0 + 16 * c;
+  const auto put = [&](int r, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 128 * r + 16 * (c ^ (r & 7))), "r"(v.x),
                  "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
+  };
+  const unsigned char *first = q + (y0 + r0) * ld + x, *last = first + 112 * ld;
+  const bool words = y0 + r0 + 112 < rows && x + 16 <= cols &&
+                     (reinterpret_cast<uintptr_t>(first) & ~uintptr_t(3)) >= reinterpret_cast<uintptr_t>(q) &&
+                     (reinterpret_cast<uintptr_t>(last) & ~uintptr_t(3)) + 20 <=
+                         reinterpret_cast<uintptr_t>(q + (rows - 1) * ld + cols);
+  if (words) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      uint32_t v[4][5], shift[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(first + 16 * (i + k) * ld);
+        const uint32_t *s = reinterpret_cast<const uint32_t *>(at & ~uintptr_t(3));
+        shift[k] = 8 * static_cast<uint32_t>(at & 3);
+#pragma unroll
+        for (int j = 0; j < 5; ++j) v[k][j] = s[j];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        put(r0 + 16 * (i + k), make_uint4(__funnelshift_r(v[k][0], v[k][1], shift[k]), __funnelshift_r(v[k][1], v[k][2], shift[k]),
+                                          __funnelshift_r(v[k][2], v[k][3], shift[k]), __funnelshift_r(v[k][3], v[k][4], shift[k])));
+    }
+  } else {
+#pragma unroll 1
+    for (int r = r0; r < 128; r += 16) put(r, load16(q, ld, rows, cols, y0 + r, x));
   }
 }
 template <class Cfg>
