@@ -26,7 +26,7 @@ bool encode_u8(CUtensorMap *m, const Fp8Operand &x, int64_t rows, int64_t cols, 
   if (!fn) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   // a single row has no stride to respect
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows == 1 ? (x.ld + 15) / 16 * 16 : x.ld)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows == 1 ? (cols + 15) / 16 * 16 : x.ld)};
   const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<unsigned char *>(x.q), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -199,7 +199,7 @@ cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s)
   // (clusters of eight were never the best: 100 x 4096 x 4096 9.7 us with four, 16.0 with eight)
   const auto tiles = [&](int n) { return tile_cycles(rows * cdiv64(p.N, 128), kb, 128, n, slots, vec, aligned); };
   const auto halves = [&](int n) { return tile_cycles(rows * cdiv64(p.N, 64), kb, 64, n, slots, vec, aligned); };
-  if (!readable) {   // one CTA an SM, and 2500 cycles a block
+  if (!readable) {   // one CTA an SM, and about three times the cycles for a block (361 us at 4096^3)
     const int n = pick_split(kb, 4, [&](int n) {
       return tile_cycles(rows * cdiv64(p.N, 128), 3 * kb, 128, n, sm_count, false, aligned);
     });

@@ -25,6 +25,15 @@
 //   LOAD: four more warps in the place of the producer
 // Every wait on an mbarrier is bounded; after giving up, a role lets its copies and
 // MMAs land (bounded) and goes to the barriers at the end.
+//
+// What bounds the pairs (256 x 256 on two SMs, the form of large products): an accumulator of 256
+// columns is handed to the epilogue and back while the only other one is filled, about 480 ns a
+// block of k, where the MMAs alone take 320; and the 1400 W of the card, reached at 8192^3 (2.4
+// PFLOP/s, 450 us; all-zero operands at the full clock 440).  Tried: four accumulators of 128 columns
+// (each MMA reads the row operand again: 345 us against 245 at 4096 x 4096 x 16384), sixteen epilogue
+// warps of 64 columns (285), the row scales through shared memory (279), four at a time (258).
+// Single CTAs (128 x 128 or 128 x 64, two an SM) read 64 KB a block and SM from the L2 cache, 20 TB/s
+// over the GPU, which bounds them at 940 cycles a block; the few-token forms stream their weights.
 #pragma once
 
 #include <cuda.h>
@@ -81,7 +90,7 @@ struct Fp8Tc {
   // FRAG: a thread holds 4 rows and every fourth pair of columns instead of one row, so it reads a
   // quarter of the column scales.  A shared memory read fills 128 bytes of registers a cycle however
   // many lanes share an address: 128 scales for each of 256 threads and block are 1024 cycles, more
-  // than the block's MMAs take (4096 x 4096 x 16384: 448 us with one row a thread, XXX so).
+  // than the block's MMAs take (4096 x 4096 x 16384: 448 us with one row a thread, 381 so).
   static constexpr bool FRAG = VEC && !SWAP && BN >= 128;
   static constexpr int CHUNK = ECOLS == 128 ? 32 : ECOLS == 64 ? 16 : ECOLS / 2;   // columns of a tensor memory load
   static_assert(ECOLS / CHUNK % 2 == 0, "chunks alternate between two buffers across blocks");
@@ -115,7 +124,7 @@ struct Fp8Tc {
                 "register split exceeds the launch budget");
   // a cluster's partial tiles, in the stage ring: lines along C's rows ([row][column], SWAP [column][row]),
   // so that a warp's reads of another CTA's are whole stretches of 64 bytes and more (16 bytes here and
-  // there took 3600 cycles instead of XXX at 24 x 8192 x 4096).  The [row][column] pitch is an odd number of
+  // there: 4100 cycles for the exchange at 24 x 8192 x 4096, so 1700).  The [row][column] pitch is an odd number of
   // 16-byte units: eight rows written at once lie in eight different ones.
   static constexpr int PART_LINES = SWAP ? BN : 128, PART_PITCH = SWAP ? 128 : BN + 4;
   static_assert(GROUP == 2 || PART_LINES * PART_PITCH * 4 <= STAGES * STAGE_BYTES, "partial tile does not fit");
@@ -214,7 +223,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
 
 // Arrive on an mbarrier of a CTA of the pair (shared::cluster address).  What the arrival hands over
 // are tensor memory reads that have completed (tcgen05.wait::ld), so it needs no release at cluster
-// scope, which would wait for every memory access of the thread: 185 -> XXX us at 4096^3.
+// scope, which would wait for every memory access of the thread: 185 -> 111 us at 4096^3.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t cbar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
@@ -628,12 +637,9 @@ __device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, i
   }
 }
 
-// One of the cluster barrier's halves: threads that have read what they want from the other CTAs arrive
-// (nothing to release: their own writes are not for the cluster), and the last wait keeps every CTA's
-// shared memory alive until all have.
-__device__ __forceinline__ void cluster_arrive_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
+// The cluster barrier's halves.  Threads that have read what they want from the other CTAs arrive (release:
+// their reads come before it), and the last wait keeps every CTA's shared memory alive until all have.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // This CTA's share (rows rank * 128 / SPLIT ..) of a tile whose partial sums lie in the shared memory of
@@ -664,7 +670,7 @@ __device__ __forceinline__ void fp8_reduce(const Fp8TcParams &p, uint32_t sbase,
       x[k][0].w += x[k][i].w;
     }
   __syncwarp();
-  cluster_arrive_relaxed();
+  cluster_arrive();
   const int line0 = Cfg::SWAP ? c0 : r0, at0 = Cfg::SWAP ? r0 : c0;
   const int lines = Cfg::SWAP ? p.cols : p.rows, length = Cfg::SWAP ? p.rows : p.cols;
   const auto store = [&](auto type) {
@@ -897,14 +903,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     __syncwarp();
     if (shared_tile) {
       cluster_sync();
-      cluster_arrive_relaxed();
+      cluster_arrive();
     }
   } else if (Cfg::LOAD && warp >= 4 + Cfg::EPI_WARPS) {
     fp8_load<Cfg>(p, sbase, bar, threadIdx.x - 128 - 32 * Cfg::EPI_WARPS);
     __syncwarp();
     if (shared_tile) {
       cluster_sync();
-      cluster_arrive_relaxed();
+      cluster_arrive();
     }
   } else {
     if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_EPI));
