@@ -739,3 +739,21 @@ def test_tensors_that_do_not_fit_are_refused(sg):
     with pytest.raises(sg.SgemmError, match="overlap"):
         x = torch.randn(128, 128, device="cuda")
         sg.sgemm_fp8_quantize(128, 128, x.data_ptr(), 0, 128, x.data_ptr(), 8, 128, s.data_ptr(), 1, 1, 128)
+
+
+# ---------------------------------------------------------------- the example
+@gpu
+def test_example_learns_and_answers(clean_status):
+    """40 steps bring the error to below a tenth (it falls until the weights' 8 bits limit it: their rounding error,
+    up to 2^-4 of a value and 2^-5.8 in the mean square, is 2e-2 of the output's unit variance at most), and tokens
+    one at a time give the rows that they give together up to BF16's last bit."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "fp8_layer.py")
+    spec = importlib.util.spec_from_file_location("fp8_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer, _, errors = example.train(tokens=1024, inputs=256, outputs=384, steps=40)
+    assert errors[-1] < errors[0] / 10
+    one, together = example.decode(layer)
+    assert ((one.float() - together.float()).abs() <= 2.0 ** -7 * together.float().abs() + 1e-6).all()
