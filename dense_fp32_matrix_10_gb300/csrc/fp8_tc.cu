@@ -11,8 +11,9 @@
 namespace sg {
 namespace {
 
-// Tensor map of a stored 8-bit matrix: boxes of 128 bytes x box_rows, 128-byte swizzle, zeros outside.
-bool encode_u8(CUtensorMap *m, const Fp8Operand &x, int64_t rows, int64_t cols, int box_rows) {
+// Tensor map of a row-major matrix of `elem`-byte elements: boxes of 128 bytes x box_rows, 128-byte swizzle, zeros
+// outside.
+bool encode_map(CUtensorMap *m, const void *base, int elem, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -26,11 +27,11 @@ bool encode_u8(CUtensorMap *m, const Fp8Operand &x, int64_t rows, int64_t cols, 
   if (!fn) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   // a single row has no stride to respect
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows == 1 ? (cols + 15) / 16 * 16 : x.ld)};
-  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<unsigned char *>(x.q), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows == 1 ? (cols * elem + 15) / 16 * 16 : ld * elem)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
+  return fn(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct KernelInfo {
@@ -96,12 +97,13 @@ cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
   t.row_qld = row.ld;
   t.col_qld = col.ld;
   t.k = p.K;
-  CUtensorMap tm_row = {}, tm_col = {};
+  CUtensorMap tm_row = {}, tm_col = {}, tm_c = {};
   const auto encode = [&](CUtensorMap *m, const Fp8Operand &x, int outer, int box) {
-    return x.inner_rows ? encode_u8(m, x, p.K, outer, 128) : encode_u8(m, x, outer, p.K, box);
+    return x.inner_rows ? encode_map(m, x.q, 1, p.K, outer, x.ld, 128) : encode_map(m, x.q, 1, outer, p.K, x.ld, box);
   };
   if (!Cfg::LOAD && (!encode(&tm_row, row, t.rows, 128) || !encode(&tm_col, col, t.cols, Cfg::BN / Cfg::GROUP)))
     return cudaErrorInvalidValue;
+  if (Cfg::BULK && !encode_map(&tm_c, p.C, 2, p.M, p.N, p.ldc, 32)) return cudaErrorInvalidValue;
   t.row_s = row.s;
   t.col_s = col.s;
   t.row_ld = row.lds;
@@ -133,10 +135,11 @@ cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
   const int64_t grid = Cfg::GROUP == 2 ? 2 * (tiles < info->clusters ? tiles : info->clusters) : tiles * split;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = launch_config<Cfg>(static_cast<unsigned>(grid), cluster, s, attr);
-  return cudaLaunchKernelEx(&cfg, fp8_tc_kernel<Cfg>, tm_row, tm_col, t);
+  return cudaLaunchKernelEx(&cfg, fp8_tc_kernel<Cfg>, tm_row, tm_col, tm_c, t);
 }
 
 using Pair = Fp8Tc<2, 256, false, false, 6, 1>;      // 256 x 256 on two SMs
+using PairBulk = Fp8Tc<2, 256, false, false, 4, 1, false, false, true>;   // the same for a C that TMA can write
 using PairStaged = Fp8Tc<2, 256, false, false, 5, 1, true>;   // the same for an unaligned C
 using PairVec = Fp8Tc<2, 256, false, true, 6, 1>;
 using Tile = Fp8Tc<1, 128, false, false, 3, 2>;      // 128 x 128, two CTAs an SM
@@ -213,6 +216,9 @@ cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s)
       1500 + cdiv64(cdiv64(p.M, 256) * cdiv64(p.N, 256), sm_count / 2) * (kb * 920 + (aligned ? 3000 : 8000));
   if (pair <= tile && pair <= half) {
     if (vec) return launch<PairVec>(p, 1, s);
+    // (a TMA store writes whole 16 bytes at the end of a row)
+    if (aligned && p.typeC != SGEMM_TYPE_F32 && p.beta == 0.0f && p.N % 8 == 0 && p.ldc < kMaxLd / 2)
+      return launch<PairBulk>(p, 1, s);
     return aligned ? launch<Pair>(p, 1, s) : launch<PairStaged>(p, 1, s);
   }
   if (half < tile) return vec ? launch<HalfVec>(p, split_half, s) : launch<Half>(p, split_half, s);

@@ -70,9 +70,9 @@ struct Fp8TcParams {
 
 // GROUP 2: a pair of CTAs computes 256 x BN (cta_group::2), each holding 128 rows and
 // half of the columns' operand.  SWAP: the tile's columns are C's rows.
-// STAGED: see below.  LOAD: four more warps read operands that TMA cannot, of any base and stride.
+// STAGED, BULK: see below.  LOAD: four more warps read operands that TMA cannot, of any base and stride.
 template <int GROUP_, int BN_, bool SWAP_, bool VEC_, int STAGES_, int CTAS_, bool STAGED_ = GROUP_ == 1,
-          bool LOAD_ = false>
+          bool LOAD_ = false, bool BULK_ = false>
 struct Fp8Tc {
   static constexpr int GROUP = GROUP_, BN = BN_, STAGES = STAGES_, CTAS = CTAS_;
   static constexpr bool SWAP = SWAP_, VEC = VEC_, LOAD = LOAD_;
@@ -106,10 +106,16 @@ struct Fp8Tc {
   // Pairs have a place for it only in the form for unaligned C: the 20 KB cost the aligned one 3 us of 74
   // at 4096^3, as the L1 cache that holds the row scales shrinks.
   static constexpr bool STAGED = STAGED_ && !SWAP && !FRAG;
-  static constexpr int STORE_PITCH = 20, STORE_BYTES = 32 * STORE_PITCH * 4;   // per warp
-  static constexpr int STORE_OFFSET = GROUP == 2 && STAGED ? SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES : 0;
+  // BULK (pairs; a C of 16 bits, beta 0, rows of whole 16 bytes): a warp writes its 32 x 128 values to shared
+  // memory as two swizzled boxes of 64 columns and leaves them to TMA stores while it goes on to the next
+  // tile.  Written by the threads a tile's stores hold its SMs up for 3 us (4096^3 74 us, XXX so).
+  static constexpr bool BULK = BULK_;
+  static_assert(!BULK || (GROUP == 2 && !VEC && !STAGED), "bulk stores: pairs with a scale per 128 columns");
+  static constexpr int STORE_PITCH = 20, STORE_BYTES = BULK ? 2 * 32 * 128 : 32 * STORE_PITCH * 4;   // per warp
+  static constexpr bool STORE_ROOM = GROUP == 2 && (STAGED || BULK);
+  static constexpr int STORE_OFFSET = STORE_ROOM ? SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES : 0;
   static constexpr int BAR_OFFSET =
-      SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES + (GROUP == 2 && STAGED ? EPI_WARPS * STORE_BYTES : 0);
+      SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES + (STORE_ROOM ? EPI_WARPS * STORE_BYTES : 0);
   static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 2 * SCALE_SLOTS + 1;
   static constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 16 + 1024;
   static_assert(VEC || BN % 64 == 0, "a thread's columns lie in one block of 128");
@@ -637,6 +643,35 @@ __device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, i
   }
 }
 
+// BULK: the same through shared memory and two TMA stores (columns and rows past the edge are not written).
+// The stores of the warp's last tile have read the place before it is written again.
+template <class Cfg, class T>
+__device__ __forceinline__ void fp8_store_bulk(const Fp8TcParams &p, const CUtensorMap *tm_c, int r, int c0, int lane,
+                                               uint32_t stage, const float (&acc)[Cfg::ECOLS]) {
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < Cfg::ECOLS; j += 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p.alpha * acc[j + i];
+    Raw<T> o;
+    pack(o, v);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + j / 64 * 4096 + 128 * lane +
+                                                                   16 * ((j % 64 / 8) ^ (lane & 7))),
+                 "r"(o.u[0].x), "r"(o.u[0].y), "r"(o.u[0].z), "r"(o.u[0].w)
+                 : "memory");
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0 && r < p.rows) {
+#pragma unroll
+    for (int j = 0; j < Cfg::ECOLS; j += 64)
+      if (c0 + j < p.cols) tma_store_2d(tm_c, stage + j / 64 * 4096, c0 + j, r);
+    bulk_commit_group();
+  }
+}
+
 // The cluster barrier's halves.  Threads that have read what they want from the other CTAs arrive (release:
 // their reads come before it), and the last wait keeps every CTA's shared memory alive until all have.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -697,7 +732,8 @@ __device__ __forceinline__ void fp8_reduce(const Fp8TcParams &p, uint32_t sbase,
 // is on its way.
 template <class Cfg>
 __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char *smem, uint32_t sbase, uint32_t tmem,
-                                             const Fp8Bars<Cfg> &bar, uint32_t rank, int q, int half, int lane) {
+                                             const Fp8Bars<Cfg> &bar, uint32_t rank, int q, int half, int lane,
+                                             const CUtensorMap *tm_c) {
   constexpr int EC = Cfg::ECOLS, CH = Cfg::CHUNK, NC = EC / CH, SB = Cfg::SCALE_BLOCKS;
   const Fp8Work<Cfg> w(p);
   const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * EC;
@@ -832,7 +868,12 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
     } else {
       const int c = c0 + half * EC, r = r0 + 32 * q;
       const uint32_t stage = sbase + Cfg::STORE_OFFSET + (q + 4 * half) * Cfg::STORE_BYTES;
-      if (p.typeC == SGEMM_TYPE_F32)
+      if constexpr (Cfg::BULK) {
+        if (p.typeC == SGEMM_TYPE_BF16)
+          fp8_store_bulk<Cfg, __nv_bfloat16>(p, tm_c, r, c, lane, stage, acc);
+        else
+          fp8_store_bulk<Cfg, __half>(p, tm_c, r, c, lane, stage, acc);
+      } else if (p.typeC == SGEMM_TYPE_F32)
         fp8_store<Cfg, float>(p, r, c, lane, stage, acc);
       else if (p.typeC == SGEMM_TYPE_BF16)
         fp8_store<Cfg, __nv_bfloat16>(p, r, c, lane, stage, acc);
@@ -840,13 +881,14 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
         fp8_store<Cfg, __half>(p, r, c, lane, stage, acc);
     }
   }
+  if (Cfg::BULK && lane == 0) bulk_wait_group_all();   // before the CTA's shared memory may go
 }
 
 // ------------------------------------------------------------------ kernel
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_row, const __grid_constant__ CUtensorMap tm_col,
-                  const __grid_constant__ Fp8TcParams p) {
+                  const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ Fp8TcParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                           ~static_cast<uintptr_t>(1023));
@@ -875,6 +917,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     if (!Cfg::LOAD) {
       tma_prefetch_desc(&tm_row);
       tma_prefetch_desc(&tm_col);
+      if (Cfg::BULK) tma_prefetch_desc(&tm_c);
     }
   }
   if (warp == 1) {
@@ -914,7 +957,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
   } else {
     if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_EPI));
-    fp8_epilogue<Cfg>(p, smem, sbase, tmem, bar, rank, warp & 3, (warp >> 2) - 1, lane);
+    fp8_epilogue<Cfg>(p, smem, sbase, tmem, bar, rank, warp & 3, (warp >> 2) - 1, lane, &tm_c);
     __syncwarp();
     if (shared_tile) {
       cluster_sync();   // every CTA's partial tile is written
