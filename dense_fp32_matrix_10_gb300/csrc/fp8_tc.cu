@@ -29,8 +29,11 @@ bool encode_map(CUtensorMap *m, const void *base, int elem, int64_t rows, int64_
   // a single row has no stride to respect
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows == 1 ? (cols * elem + 15) / 16 * 16 : ld * elem)};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
-  return fn(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base),
-            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(m,
+            elem == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+            : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+            2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -83,6 +86,8 @@ const KernelInfo *kernel_info() {
   return i.err == cudaSuccess ? &i : nullptr;
 }
 
+int size_of(int type) { return type == SGEMM_TYPE_F32 ? 4 : 2; }
+
 // `split`: CTAs per tile (GROUP == 1).
 template <class Cfg>
 cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
@@ -103,7 +108,7 @@ cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
   };
   if (!Cfg::LOAD && (!encode(&tm_row, row, t.rows, 128) || !encode(&tm_col, col, t.cols, Cfg::BN / Cfg::GROUP)))
     return cudaErrorInvalidValue;
-  if (Cfg::BULK && !encode_map(&tm_c, p.C, 2, p.M, p.N, p.ldc, 32)) return cudaErrorInvalidValue;
+  if (Cfg::BULK && !encode_map(&tm_c, p.C, size_of(p.typeC), p.M, p.N, p.ldc, 32)) return cudaErrorInvalidValue;
   t.row_s = row.s;
   t.col_s = col.s;
   t.row_ld = row.lds;
@@ -126,7 +131,7 @@ cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
   t.C = p.C;
   t.ldc = p.ldc;
   t.typeC = p.typeC;
-  t.vecC = aligned_rows(p.C, p.ldc, p.typeC == SGEMM_TYPE_F32 ? 4 : 2, 16);
+  t.vecC = aligned_rows(p.C, p.ldc, size_of(p.typeC), 16);
   t.alpha = p.alpha;
   t.beta = p.beta;
   t.wait_budget_ns = p.wait_budget_ns;
@@ -141,7 +146,8 @@ cudaError_t launch(const Fp8Params &p, int split, cudaStream_t s) {
 using Pair = Fp8Tc<2, 256, false, false, 6, 1>;      // 256 x 256 on two SMs
 using PairBulk = Fp8Tc<2, 256, false, false, 4, 1, false, false, true>;   // the same for a C that TMA can write
 using PairStaged = Fp8Tc<2, 256, false, false, 5, 1, true>;   // the same for an unaligned C
-using PairVec = Fp8Tc<2, 256, false, true, 6, 1>;
+using PairVec = Fp8Tc<2, 256, false, true, 6, 1, false>;
+using PairVecBulk = Fp8Tc<2, 256, false, true, 4, 1, false, false, true>;
 using Tile = Fp8Tc<1, 128, false, false, 3, 2>;      // 128 x 128, two CTAs an SM
 using TileVec = Fp8Tc<1, 128, false, true, 3, 2>;
 using Half = Fp8Tc<1, 64, false, false, 3, 2>;       // 128 x 64
@@ -197,7 +203,7 @@ cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s)
     if (cols == 16) return launch<Few16>(p, split, s);
     return cols == 32 ? launch<Few32>(p, split, s) : launch<Few64>(p, split, s);
   }
-  const bool vec = p.b.shift == 0, aligned = aligned_rows(p.C, p.ldc, p.typeC == SGEMM_TYPE_F32 ? 4 : 2, 16);
+  const bool vec = p.b.shift == 0, aligned = aligned_rows(p.C, p.ldc, size_of(p.typeC), 16);
   const int64_t rows = cdiv64(p.M, 128);
   // (clusters of eight were never the best: 100 x 4096 x 4096 9.7 us with four, 16.0 with eight)
   const auto tiles = [&](int n) { return tile_cycles(rows * cdiv64(p.N, 128), kb, 128, n, slots, vec, aligned); };
@@ -215,10 +221,11 @@ cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s)
   const int64_t pair =
       1500 + cdiv64(cdiv64(p.M, 256) * cdiv64(p.N, 256), sm_count / 2) * (kb * 920 + (aligned ? 3000 : 8000));
   if (pair <= tile && pair <= half) {
-    if (vec) return launch<PairVec>(p, 1, s);
     // (a TMA store writes whole 16 bytes at the end of a row)
-    if (aligned && p.typeC != SGEMM_TYPE_F32 && p.beta == 0.0f && p.N % 8 == 0 && p.ldc < kMaxLd / 2)
-      return launch<PairBulk>(p, 1, s);
+    const int size = size_of(p.typeC);
+    const bool bulk = aligned && p.beta == 0.0f && static_cast<int64_t>(p.N) * size % 16 == 0 && p.ldc < kMaxLd / size;
+    if (vec) return bulk ? launch<PairVecBulk>(p, 1, s) : launch<PairVec>(p, 1, s);
+    if (bulk) return launch<PairBulk>(p, 1, s);
     return aligned ? launch<Pair>(p, 1, s) : launch<PairStaged>(p, 1, s);
   }
   if (half < tile) return vec ? launch<HalfVec>(p, split_half, s) : launch<Half>(p, split_half, s);

@@ -106,11 +106,12 @@ struct Fp8Tc {
   // Pairs have a place for it only in the form for unaligned C: the 20 KB cost the aligned one 3 us of 74
   // at 4096^3, as the L1 cache that holds the row scales shrinks.
   static constexpr bool STAGED = STAGED_ && !SWAP && !FRAG;
-  // BULK (pairs; a C of 16 bits, beta 0, rows of whole 16 bytes): a warp writes its 32 x 128 values to shared
-  // memory as two swizzled boxes of 64 columns and leaves them to TMA stores while it goes on to the next
-  // tile.  Written by the threads a tile's stores hold its SMs up for 3 us (4096^3 74 us, XXX so).
+  // BULK (pairs; beta 0, rows of C of whole 16 bytes): a warp writes its 32 x 128 values, or 32 x 64 of F32 at a
+  // time, to shared memory as swizzled boxes of 128-byte rows and leaves them to TMA stores while it goes on
+  // to the next tile.  Written by the threads, a tile's stores hold its SMs up for 3 us (4096^3 in BF16
+  // 73.1 us, so 64.3).
   static constexpr bool BULK = BULK_;
-  static_assert(!BULK || (GROUP == 2 && !VEC && !STAGED), "bulk stores: pairs with a scale per 128 columns");
+  static_assert(!BULK || (GROUP == 2 && !STAGED), "bulk stores: pairs");
   static constexpr int STORE_PITCH = 20, STORE_BYTES = BULK ? 2 * 32 * 128 : 32 * STORE_PITCH * 4;   // per warp
   static constexpr bool STORE_ROOM = GROUP == 2 && (STAGED || BULK);
   static constexpr int STORE_OFFSET = STORE_ROOM ? SCALE_OFFSET + SCALE_SLOTS * SCALE_BYTES : 0;
@@ -643,32 +644,54 @@ __device__ __forceinline__ void fp8_store(const Fp8TcParams &p, int r, int c0, i
   }
 }
 
-// BULK: the same through shared memory and two TMA stores (columns and rows past the edge are not written).
-// The stores of the warp's last tile have read the place before it is written again.
+// BULK: the same through shared memory and TMA stores (columns and rows past the edge are not written).  The
+// warp's last stores have read the place before it is written again.
 template <class Cfg, class T>
 __device__ __forceinline__ void fp8_store_bulk(const Fp8TcParams &p, const CUtensorMap *tm_c, int r, int c0, int lane,
                                                uint32_t stage, const float (&acc)[Cfg::ECOLS]) {
-  if (lane == 0) bulk_wait_group_read<0>();
-  __syncwarp();
+  constexpr int BOX = 128 / sizeof(T), COLS = Cfg::STORE_BYTES / 32 / sizeof(T);   // columns of a box, of a pass
+  // column `col` of the pass and row `row`: boxes of 32 rows, 16-byte units exchanged as the map's swizzle does
+  const auto place = [&](int row, int col) {
+    const int unit = col % BOX * static_cast<int>(sizeof(T)) / 16, rest = col * static_cast<int>(sizeof(T)) % 16;
+    return stage + col / BOX * 4096 + 128 * row + 16 * (unit ^ (row & 7)) + rest;
+  };
 #pragma unroll
-  for (int j = 0; j < Cfg::ECOLS; j += 8) {
-    float v[8];
+  for (int j0 = 0; j0 < Cfg::ECOLS; j0 += COLS) {
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+    if constexpr (Cfg::FRAG) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = p.alpha * acc[j + i];
-    Raw<T> o;
-    pack(o, v);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + j / 64 * 4096 + 128 * lane +
-                                                                   16 * ((j % 64 / 8) ^ (lane & 7))),
-                 "r"(o.u[0].x), "r"(o.u[0].y), "r"(o.u[0].z), "r"(o.u[0].w)
-                 : "memory");
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0 && r < p.rows) {
+      for (int j = 0; j < COLS; j += 2) {
+        const uint32_t to = place(frag_row<Cfg>(j0 + j, lane), frag_col<Cfg>(j0 + j, lane) - j0);
+        const float v0 = p.alpha * acc[j0 + j], v1 = p.alpha * acc[j0 + j + 1];
+        if constexpr (sizeof(T) == 4)
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v0), "f"(v1) : "memory");
+        else
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(pack2(v0, v1, T())) : "memory");
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < Cfg::ECOLS; j += 64)
-      if (c0 + j < p.cols) tma_store_2d(tm_c, stage + j / 64 * 4096, c0 + j, r);
-    bulk_commit_group();
+      for (int j = 0; j < COLS; j += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = p.alpha * acc[j0 + j + i];
+        Raw<T> o;
+        pack(o, v);
+#pragma unroll
+        for (int u = 0; u < static_cast<int>(sizeof(o) / 16); ++u)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(lane, j + 4 * u)), "r"(o.u[u].x),
+                       "r"(o.u[u].y), "r"(o.u[u].z), "r"(o.u[u].w)
+                       : "memory");
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && r < p.rows) {
+#pragma unroll
+      for (int j = 0; j < COLS; j += BOX)
+        if (c0 + j0 + j < p.cols) tma_store_2d(tm_c, stage + j / BOX * 4096, c0 + j0 + j, r);
+      bulk_commit_group();
+    }
   }
 }
 
@@ -869,7 +892,9 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
       const int c = c0 + half * EC, r = r0 + 32 * q;
       const uint32_t stage = sbase + Cfg::STORE_OFFSET + (q + 4 * half) * Cfg::STORE_BYTES;
       if constexpr (Cfg::BULK) {
-        if (p.typeC == SGEMM_TYPE_BF16)
+        if (p.typeC == SGEMM_TYPE_F32)
+          fp8_store_bulk<Cfg, float>(p, tm_c, r, c, lane, stage, acc);
+        else if (p.typeC == SGEMM_TYPE_BF16)
           fp8_store_bulk<Cfg, __nv_bfloat16>(p, tm_c, r, c, lane, stage, acc);
         else
           fp8_store_bulk<Cfg, __half>(p, tm_c, r, c, lane, stage, acc);
