@@ -90,9 +90,9 @@ struct Fp8Tc {
   // FRAG: a thread holds 4 rows and every fourth pair of columns instead of one row, so it reads a
   // quarter of the column scales.  A shared memory read fills 128 bytes of registers a cycle however
   // many lanes share an address: 128 scales for each of 256 threads and block are 1024 cycles, more
-  // than the block's MMAs take (4096 x 4096 x 16384: 448 us with one row a thread, 381 so).
+  // than the block's MMAs take (4096 x 4096 x 16384: 448 us with one row a thread, 363 so).
   static constexpr bool FRAG = VEC && !SWAP && BN >= 128;
-  static constexpr int CHUNK = ECOLS == 128 ? 32 : ECOLS == 64 ? 16 : ECOLS / 2;   // columns of a tensor memory load
+  static constexpr int CHUNK = ECOLS == 128 && !FRAG ? 32 : ECOLS >= 64 ? 16 : ECOLS / 2;   // columns of a tensor memory load
   static_assert(ECOLS / CHUNK % 2 == 0, "chunks alternate between two buffers across blocks");
   // VEC: ring of scales, SCALE_BLOCKS blocks of k a slot (one wait per slot, not per block): the rows'
   // [row][block], then the columns' [block][column]
@@ -235,24 +235,11 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t cbar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
 
-// FRAG: 32 rows x 32 or 16 columns in pieces of 8 x 2 per four lanes.  With H registers for either half of
-// the 32 TMEM lanes, lane l gets rows l / 4 + 8 i and columns 8 n + 2 (l % 4) + {0, 1} in
-// v[H (i / 2) + 4 n + 2 (i % 2) + {0, 1}].
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&v)[32]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {   // lanes 0..15, 16..31
-    uint32_t *o = v + 16 * h;
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-          "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-        : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16)));
-  }
-}
+// FRAG: 32 rows x 16 columns in pieces of 8 x 2 per four lanes: lane l gets rows l / 4 + 8 i and columns
+// 8 n + 2 (l % 4) + {0, 1} in v[8 (i / 2) + 4 n + 2 (i % 2) + {0, 1}].
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&v)[16]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 2; ++h) {   // lanes 0..15, 16..31
     uint32_t *o = v + 8 * h;
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7])
@@ -750,9 +737,10 @@ __device__ __forceinline__ void fp8_reduce(const Fp8TcParams &p, uint32_t sbase,
 }
 
 // ------------------------------------------------------------------ epilogue
-// The loads of tensor memory run one chunk ahead of the sums, across blocks too: before the last
-// chunk of a block is added, its accumulator has been handed back and the next block's first chunk
-// is on its way.
+// The loads of tensor memory run one chunk ahead of the sums, across blocks too: before the last chunk of a
+// block is added, its accumulator has been handed back and the next block's first chunk is on its way.  (FRAG:
+// a chunk's scales are multiplied while its own load is on its way, which takes as long; 381 -> 363 us at
+// 4096 x 4096 x 16384.)
 template <class Cfg>
 __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char *smem, uint32_t sbase, uint32_t tmem,
                                              const Fp8Bars<Cfg> &bar, uint32_t rank, int q, int half, int lane,
@@ -789,26 +777,25 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
     }
     if (w.kb0 < w.kb1) {
       if (!acc_ready(it)) return;
-      tmem_ld_chunk<Cfg>(src + it % Cfg::ACCS * Cfg::BN, v[0]);
+      if (!Cfg::FRAG) tmem_ld_chunk<Cfg>(src + it % Cfg::ACCS * Cfg::BN, v[0]);
     }
-    for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+    const float *sc = nullptr;   // VEC: the block's scales
+    for (int kb = w.kb0, i = 0; kb < w.kb1; ++kb, ++it) {   // i: block of its slot of scales
       const uint32_t b = it % Cfg::ACCS;
       const bool more = kb + 1 < w.kb1;
-      const int i = (kb - w.kb0) % SB;
-      const uint32_t slot = group % (Cfg::VEC ? Cfg::SCALE_SLOTS : 1);
-      const float *sc = reinterpret_cast<const float *>(smem + Cfg::SCALE_OFFSET + slot * Cfg::SCALE_BYTES);
       float2 rs[4];   // FRAG: the scales of the thread's four rows; else of its one
       if constexpr (Cfg::VEC) {
         if (i == 0) {
+          const uint32_t slot = group % Cfg::SCALE_SLOTS;
           const bool ok = wait_parity_bounded(bar.sc_full(slot), group / Cfg::SCALE_SLOTS & 1, p.wait_budget_ns, p.status);
           if (!__all_sync(~0u, ok)) return;
+          sc = reinterpret_cast<const float *>(smem + Cfg::SCALE_OFFSET + slot * Cfg::SCALE_BYTES);
         }
 #pragma unroll
         for (int j = 0; j < (Cfg::FRAG ? 4 : 1); ++j) {
           const float f = sc[(Cfg::FRAG ? 32 * q + lane / 4 + 8 * j : row) * SB + i];
           rs[j] = make_float2(f, f);
         }
-        sc += Cfg::COL_SCALES + i * Cfg::BN + half * EC;
       } else {
         const float f = row_s * col_s;
         rs[0] = make_float2(f, f);
@@ -817,26 +804,31 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
           col_s = *(cp += cstep);
         }
       }
+      const float *cols = sc + Cfg::COL_SCALES + i * Cfg::BN + half * EC;
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc) {
-        uint32_t(&x)[CH] = v[cc & 1];
+        uint32_t(&x)[CH] = v[Cfg::FRAG ? 0 : cc & 1];
+        if constexpr (Cfg::FRAG) tmem_ld_chunk<Cfg>(src + b * Cfg::BN + cc * CH, x);
         // the columns' scales, before the values are there: of the chunk's columns, or (FRAG) of the
-        // thread's four pairs of them
+        // thread's pairs of them, times its rows'
         float2 f[CH / 2];
         if constexpr (Cfg::FRAG) {
+          float2 u[CH / 8];
 #pragma unroll
-          for (int n = 0; n < CH / 8; ++n) f[n] = *reinterpret_cast<const float2 *>(sc + cc * CH + 8 * n + 2 * (lane & 3));
+          for (int n = 0; n < CH / 8; ++n) u[n] = *reinterpret_cast<const float2 *>(cols + cc * CH + 8 * n + 2 * (lane & 3));
+#pragma unroll
+          for (int j = 0; j < CH; j += 2) f[j / 2] = __fmul2_rn(u[j % (CH / 2) / 4], rs[j / (CH / 2) * 2 + j / 2 % 2]);
         } else if constexpr (Cfg::VEC) {
 #pragma unroll
           for (int j = 0; j < CH; j += 4) {
-            const float4 u = *reinterpret_cast<const float4 *>(sc + cc * CH + j);
+            const float4 u = *reinterpret_cast<const float4 *>(cols + cc * CH + j);
             f[j / 2] = __fmul2_rn(make_float2(u.x, u.y), rs[0]);
             f[j / 2 + 1] = __fmul2_rn(make_float2(u.z, u.w), rs[0]);
           }
         }
         tmem_ld_wait_for(x);
         if (cc + 1 < NC) {
-          tmem_ld_chunk<Cfg>(src + b * Cfg::BN + (cc + 1) * CH, v[(cc + 1) & 1]);
+          if (!Cfg::FRAG) tmem_ld_chunk<Cfg>(src + b * Cfg::BN + (cc + 1) * CH, v[(cc + 1) & 1]);
         } else {
           tc_fence_before_sync();
           __syncwarp();
@@ -848,26 +840,25 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
           }
           if (more) {
             if (!acc_ready(it + 1)) return;
-            tmem_ld_chunk<Cfg>(src + (it + 1) % Cfg::ACCS * Cfg::BN, v[0]);
+            if (!Cfg::FRAG) tmem_ld_chunk<Cfg>(src + (it + 1) % Cfg::ACCS * Cfg::BN, v[0]);
           }
         }
 #pragma unroll
         for (int j = 0; j < CH; j += 2) {
           float *o = acc + cc * CH + j;
           const float2 a = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-          const float2 c = Cfg::FRAG  ? __fmul2_rn(f[j % (CH / 2) / 4], rs[j / (CH / 2) * 2 + j / 2 % 2])
-                           : Cfg::VEC ? f[j / 2]
-                                      : rs[0];
+          const float2 c = Cfg::VEC ? f[j / 2] : rs[0];
           const float2 sum = __ffma2_rn(a, c, make_float2(o[0], o[1]));
           o[0] = sum.x;
           o[1] = sum.y;
         }
       }
       if constexpr (Cfg::VEC) {
-        if (!more || i == SB - 1) {
+        if (++i == SB || !more) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar.sc_empty(slot));
+          if (lane == 0) mbar_arrive(bar.sc_empty(group % Cfg::SCALE_SLOTS));
           ++group;
+          i = 0;
         }
       }
     }

@@ -75,11 +75,8 @@ at::Tensor empty(at::IntArrayRef sizes, const Matrix &like, at::ScalarType type)
 }
 // rows x cols 8-bit elements, rows on 16-byte boundaries.
 at::Tensor empty_fp8(int64_t rows, int64_t cols, const Matrix &like, at::ScalarType type, int64_t &ld) {
-  ld = (cols + 15) / 16 * 16;
-  at::Tensor t = empty({rows, ld}, like, type);
-  if (ld != cols) t = t.narrow(1, 0, cols);
-  ld = at_least_1(ld);
-  return t;
+  ld = at_least_1((cols + 15) / 16 * 16);
+  return at::empty_strided({rows, cols}, {ld, 1}, like.t->options().dtype(type));
 }
 // The block along the outer dimension that an operand's scales stand for (0: they do not fit).
 int scale_block(const Matrix &s, int64_t outer, int64_t kb, bool inner_rows) {

@@ -183,9 +183,8 @@ def _cdiv(a, b):
 
 def _empty_fp8(rows, cols, dtype, dev):
     """(tensor, ld): rows on 16-byte boundaries."""
-    ld = (cols + 15) // 16 * 16
-    t = torch.empty((rows, ld), dtype=dtype, device=dev)
-    return (t if ld == cols else t[:, :cols]), max(ld, 1)
+    ld = max((cols + 15) // 16 * 16, 1)
+    return torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=dev), ld
 
 
 def _fp8_type(dtype):
