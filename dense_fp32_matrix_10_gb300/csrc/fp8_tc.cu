@@ -167,9 +167,8 @@ bool tma_readable(const Fp8Operand &x, int64_t stored_rows) {
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Cycles that a product of `tiles` tiles of 128 x cols takes with `split` CTAs a tile, two CTAs an SM, as
-// measured: 960 for a block of k (the copies from the L2 cache bound either width; 1150 with a scale per
-// column), 4000 for a CTA's first copies and its stores (more where C's rows are unaligned), and the exchange
-// of partial tiles.
+// measured: 960 for a block of k of either width (1150 with a scale per column), 4000 for a CTA's first copies
+// and its stores (more where C's rows are unaligned), and the exchange of partial tiles.
 int64_t tile_cycles(int64_t tiles, int64_t kblocks, int cols, int split, int64_t slots, bool vec, bool aligned) {
   const int64_t store = split > 1 ? 1500 + 40 * cols : aligned ? 0 : 40 * cols;
   return cdiv64(tiles * split, slots) * (cdiv64(kblocks, split) * (vec ? 1150 : 960) + 4000 + store);

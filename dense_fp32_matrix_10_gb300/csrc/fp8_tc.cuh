@@ -27,13 +27,13 @@
 // MMAs land (bounded) and goes to the barriers at the end.
 //
 // What bounds the pairs (256 x 256 on two SMs, the form of large products): an accumulator of 256
-// columns is handed to the epilogue and back while the only other one is filled, about 480 ns a
-// block of k, where the MMAs alone take 320; and the 1400 W of the card, reached at 8192^3 (2.4
-// PFLOP/s, 450 us; all-zero operands at the full clock 440).  Tried: four accumulators of 128 columns
-// (each MMA reads the row operand again: 345 us against 245 at 4096 x 4096 x 16384), sixteen epilogue
+// columns is handed to the epilogue and back while the only other one is filled, about 450 ns a
+// block of k, where the MMAs alone take 320; and the 1400 W of the card, reached in sustained runs of
+// 8192^3 (2.5 PFLOP/s, 448 us; 401 in short ones).  Tried, at 4096 x 4096 x 16384 in 245 us then: four
+// accumulators of 128 columns (345; such an MMA takes nearly as long as one of 256), sixteen epilogue
 // warps of 64 columns (285), the row scales through shared memory (279), four at a time (258).
-// Single CTAs (128 x 128 or 128 x 64, two an SM) read 64 KB a block and SM from the L2 cache, 20 TB/s
-// over the GPU, which bounds them at 940 cycles a block; the few-token forms stream their weights.
+// Single CTAs (128 x 128 or 128 x 64, two an SM) are bound the same way (512 x 4096 x 8192 25.2 us, without
+// any copies 22.8), the few-token forms by their weights' way from memory and by latencies.
 #pragma once
 
 #include <cuda.h>
@@ -779,7 +779,7 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
       if (!acc_ready(it)) return;
       if (!Cfg::FRAG) tmem_ld_chunk<Cfg>(src + it % Cfg::ACCS * Cfg::BN, v[0]);
     }
-    const float *sc = nullptr;   // VEC: the block's scales
+    const float *sc = reinterpret_cast<const float *>(smem + Cfg::SCALE_OFFSET);   // VEC: the slot's scales
     for (int kb = w.kb0, i = 0; kb < w.kb1; ++kb, ++it) {   // i: block of its slot of scales
       const uint32_t b = it % Cfg::ACCS;
       const bool more = kb + 1 < w.kb1;
