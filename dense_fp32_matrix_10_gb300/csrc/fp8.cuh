@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -40,6 +41,15 @@ __device__ __forceinline__ uint32_t to_fp8x2(float x0, float x1) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
   return r;
 }
+// x / s from inv = 1 / s: the product with inv and one correction by its remainder, which an FMA gives exactly.
+// The product alone is up to one and a half units in the last place off, and then falls on the other side of a
+// midpoint between two 8-bit values three times as often as the rounded quotient does.
+// s comes from divisor(): of an infinite scale it is 0, so that a finite x over it stays 0 (0 * inf would be NaN).
+__device__ __forceinline__ float divisor(float scale) { return scale < INFINITY ? scale : 0.0f; }
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  const float q = x * inv;
+  return fmaf(fmaf(-q, s, x), inv, q);
+}
 __device__ __forceinline__ uint2 to_fp8x8(const float (&v)[8], float mul, bool e5m2) {
   uint2 u;
   if (e5m2) {
@@ -51,6 +61,14 @@ __device__ __forceinline__ uint2 to_fp8x8(const float (&v)[8], float mul, bool e
   }
   return u;
 }
+// Eight elements of one block.
+__device__ __forceinline__ uint2 quantize8(const float (&v)[8], float s, float inv, bool e5m2) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s, inv);
+  return to_fp8x8(q, 1.0f, e5m2);
+}
+
 // ------------------------------------------------------------ F32, BF16, F16
 // Raw<T>: eight consecutive elements as loaded.
 template <class T> struct Raw;

@@ -66,15 +66,16 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
   if (MODE & kRow) {
     // each lane divides for the row that it owns
     const int mine = owned(lane16);
-    const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), inv = __fdiv_rn(1.0f, s);
+    const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), inv = __fdiv_rn(1.0f, s), div = divisor(s);
     if ((lane16 & 1) == 0 && 16 * mine < rows) p.sr[(r0 + 16 * mine) * p.ldsr + tc] = s;
     unsigned char *q = p.qr + r0 * p.ldqr + c0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float f = __shfl_sync(~0u, inv, (i & 4) * 2 + (i & 2) * 2 + (i & 1) * 2, 16);
+      const int from = (i & 4) * 2 + (i & 2) * 2 + (i & 1) * 2;
+      const float si = __shfl_sync(~0u, div, from, 16), fi = __shfl_sync(~0u, inv, from, 16);
       float v[8];
       unpack(raw[i], v);
-      if (16 * i < rows) store8_fp8(q + 16 * i * p.ldqr, to_fp8x8(v, f, p.e5m2), n, vec_r);
+      if (16 * i < rows) store8_fp8(q + 16 * i * p.ldqr, quantize8(v, si, fi, p.e5m2), n, vec_r);
     }
   }
   if (MODE & kTile) {
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
       float v[8];
       unpack(raw[i], v);
       if (16 * i < rows)
-        store8_fp8(p.qr + (r0 + 16 * i) * p.ldqr + c0, to_fp8x8(v, inv, p.e5m2), n, vec_r);
+        store8_fp8(p.qr + (r0 + 16 * i) * p.ldqr + c0, quantize8(v, divisor(s), inv, p.e5m2), n, vec_r);
     }
   }
   if (MODE & kCol) {
@@ -113,17 +114,21 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
       const int64_t c = tc * 128 + threadIdx.x;
       if (c < p.cols) p.sc[tr * p.ldsc + c] = s;
       part[0][threadIdx.x] = __fdiv_rn(1.0f, s);
+      part[1][threadIdx.x] = divisor(s);
     }
     __syncthreads();
-    float inv[8];
+    float inv[8], scale[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) inv[j] = part[0][lane16 * 8 + j];
+    for (int j = 0; j < 8; ++j) {
+      inv[j] = part[0][lane16 * 8 + j];
+      scale[j] = part[1][lane16 * 8 + j];
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float v[8];
       unpack(raw[i], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= inv[j];
+      for (int j = 0; j < 8; ++j) v[j] = quotient(v[j], scale[j], inv[j]);
       if (16 * i < rows)
         store8_fp8(p.qc + (r0 + 16 * i) * p.ldqc + c0, to_fp8x8(v, 1.0f, p.e5m2), n, vec_c);
     }
@@ -132,8 +137,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
 
 // Both quantisations of 16-bit elements.  In registers (as above) the tile, its maxima and their use took 117
 // registers and two CTAs an SM, too few bytes in flight (16384 x 8192 116 us, 4.6 TB/s); here the tile lies in
-// shared memory, put there by asynchronous copies, and five CTAs fit (92 us, 5.8 TB/s).  Of F32, whose tile takes
-// twice the room, the registers are as fast (4096 x 8192 38 against 42 us).
+// shared memory, put there by asynchronous copies, and five CTAs fit (92 us; 108 with the corrected quotients that
+// both forms have since).  Of F32, whose tile takes twice the room, the registers are as fast (4096 x 8192 38
+// against 42 us).
 template <class T>
 __global__ void __launch_bounds__(256, 5)
     quantize_both_kernel(const QuantizeParams p, const int64_t tiles_c, const bool vec_x, const bool vec_r,
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(256, 5)
     for (int j = 0; j < 8; ++j) rmax[i] = max_abs(rmax[i], v[j]);
   }
   const int own = owned(lane16);
-  const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), row_inv = __fdiv_rn(1.0f, s);
+  const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), row_inv = __fdiv_rn(1.0f, s), div = divisor(s);
   if ((lane16 & 1) == 0 && 16 * own < rows) p.sr[(r0 + 16 * own) * p.ldsr + tc] = s;
   __syncthreads();
   if (threadIdx.x < 128) {
@@ -202,21 +208,26 @@ __global__ void __launch_bounds__(256, 5)
     const int64_t c = tc * 128 + threadIdx.x;
     if (c < p.cols) p.sc[tr * p.ldsc + c] = t;
     part[0][threadIdx.x] = __fdiv_rn(1.0f, t);
+    part[1][threadIdx.x] = divisor(t);
   }
   __syncthreads();
-  float inv[8];
+  float inv[8], scale[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) inv[j] = part[0][lane16 * 8 + j];
+  for (int j = 0; j < 8; ++j) {
+    inv[j] = part[0][lane16 * 8 + j];
+    scale[j] = part[1][lane16 * 8 + j];
+  }
   unsigned char *qr = p.qr + r0 * p.ldqr + c0, *qc = p.qc + r0 * p.ldqc + c0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float f = __shfl_sync(~0u, row_inv, (i & 4) * 2 + (i & 2) * 2 + (i & 1) * 2, 16);
+    const int from = (i & 4) * 2 + (i & 2) * 2 + (i & 1) * 2;
+    const float si = __shfl_sync(~0u, div, from, 16), fi = __shfl_sync(~0u, row_inv, from, 16);
     float v[8];
     unpack(load8(mine + 16 * i * PITCH, 8, true), v);
     if (16 * i < rows) {
-      store8_fp8(qr + 16 * i * p.ldqr, to_fp8x8(v, f, p.e5m2), n, vec_r);
+      store8_fp8(qr + 16 * i * p.ldqr, quantize8(v, si, fi, p.e5m2), n, vec_r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= inv[j];
+      for (int j = 0; j < 8; ++j) v[j] = quotient(v[j], scale[j], inv[j]);
       store8_fp8(qc + 16 * i * p.ldqc, to_fp8x8(v, 1.0f, p.e5m2), n, vec_c);
     }
   }

@@ -77,7 +77,7 @@ SGEMM_API sgemm_status_t sgemm_fp8(int transA, int transB, int64_t M, int64_t N,
  * block_cols, which are 1 x 128, 128 x 1 or 128 x 128: with a the largest |x|
  * of a block,
  *
- *   s = max(a / F, 2^-126),    q = x * (1 / s) rounded to nearest even.
+ *   s = max(a / F, 2^-126),    q = x / s rounded to nearest even.
  *
  * A block of zeros has q = 0 and the least scale.  A block that holds a NaN or
  * an infinity has that as its scale, so that whatever the product makes of it
@@ -103,7 +103,7 @@ SGEMM_API sgemm_status_t sgemm_fp8_quantize_both(int64_t rows, int64_t cols, con
  * RMS norm of x + r with an 8-bit output, row by row:
  *
  *   h = x + r,   t = 1 / sqrt(mean(h^2) + eps),   y = h * t * w,
- *   (q, s) = y quantised in 1 x 128 blocks (sgemm_fp8_quantize)
+ *   (q, s) = y quantised in 1 x 128 blocks (sgemm_fp8_quantize; q = y * (1 / s) here)
  *
  * X and R (NULL: h = x) are rows x cols of typeX (F32, BF16, F16), W has cols
  * elements of typeW (F32 or typeX).  Q and S are always written; H and Y (of

@@ -177,6 +177,24 @@ def test_quantise_special_values(sg, block):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_quantise_finite_beside_an_infinity(sg, dtype):
+    """x / inf is 0 for the block's finite elements, and NaN only where x is infinite."""
+    x = torch.randn(256, 256, generator=rng(15), device="cuda").to(dtype)
+    x[3, 5] = float("inf")
+    qr, _, qc, _ = sg.quantize_fp8_both(x)
+    t = sg.quantize_fp8(x, (B, B))
+    for q, inside in ((qr, (slice(3, 4), slice(0, B))), (sg.quantize_fp8(x)[0], (slice(3, 4), slice(0, B))),
+                      (qc, (slice(0, B), slice(5, 6))), (sg.quantize_fp8(x, (B, 1))[0], (slice(0, B), slice(5, 6))),
+                      (t[0], (slice(0, B), slice(0, B)))):
+        v = q.float()
+        assert torch.isnan(v[3, 5])
+        v[3, 5] = 0
+        assert (v[inside] == 0).all()
+        assert torch.isfinite(v).all() and (v != 0).any()
+
+
+@gpu
 def test_quantise_beyond_32_bit_offsets(sg):
     rows, cols, ld = 70000, 136, 32768
     buf = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda")
