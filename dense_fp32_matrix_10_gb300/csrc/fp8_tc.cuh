@@ -319,7 +319,7 @@ __device__ __forceinline__ void fp8_produce(const Fp8TcParams &p, const CUtensor
       }
     }
   }
-  if (!ok && rank == 0) {   // the copies in flight land before the CTA may end
+  if (rank == 0) {   // the copies in flight land before the CTA may end, whichever role gave up
     for (uint32_t j = it > Cfg::STAGES ? it - Cfg::STAGES : 0; j < it; ++j)
       wait_parity_bounded(bar.full(j % Cfg::STAGES), (j / Cfg::STAGES) & 1, p.wait_budget_ns, nullptr);
   }
@@ -897,7 +897,6 @@ __device__ __forceinline__ void fp8_epilogue(const Fp8TcParams &p, unsigned char
         fp8_store<Cfg, __half>(p, r, c, lane, stage, acc);
     }
   }
-  if (Cfg::BULK && lane == 0) bulk_wait_group_all();   // before the CTA's shared memory may go
 }
 
 // ------------------------------------------------------------------ kernel
@@ -974,7 +973,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
   } else {
     if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_EPI));
     fp8_epilogue<Cfg>(p, smem, sbase, tmem, bar, rank, warp & 3, (warp >> 2) - 1, lane, &tm_c);
+    // whatever ended the epilogue: its stores are done with this CTA's shared memory, and its loads with the
+    // tensor memory, before those may go
+    if (Cfg::BULK && lane == 0) bulk_wait_group_all();
     __syncwarp();
+    tmem_ld_wait();
     if (shared_tile) {
       cluster_sync();   // every CTA's partial tile is written
       int r0, c0;
