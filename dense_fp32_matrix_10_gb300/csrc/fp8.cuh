@@ -41,14 +41,18 @@ __device__ __forceinline__ uint32_t to_fp8x2(float x0, float x1) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
   return r;
 }
-// x / s from inv = 1 / s: the product with inv and one correction by its remainder, which an FMA gives exactly.
-// The product alone is up to one and a half units in the last place off, and then falls on the other side of a
-// midpoint between two 8-bit values three times as often as the rounded quotient does.
+// x / s from ninv = -1 / s: the product and one correction by its remainder, which an FMA gives exactly.
+// The product alone is up to one and a half units in the last place off.  Where x has few bits its quotient by
+// max / F often is a midpoint between two 8-bit values, which the product then leaves for the wrong side: of 42 million
+// BF16 values in E4M3 21072 differed from the definition in 64 bits, 661 with the correction and with an FP32 division
+// alike, which two agreed in every value (F16 2454 and 131; F32 24 and 21).
+// Of -x and -1 / s, since a remainder of zero is then taken off a quotient of -0, which keeps its sign (with every
+// sign the other way round it is added; negating the remainder instead cost 22.8 us for 21.3 at 4095 x 4104 both ways).
 // s comes from divisor(): of an infinite scale it is 0, so that a finite x over it stays 0 (0 * inf would be NaN).
 __device__ __forceinline__ float divisor(float scale) { return scale < INFINITY ? scale : 0.0f; }
-__device__ __forceinline__ float quotient(float x, float s, float inv) {
-  const float q = x * inv;
-  return fmaf(fmaf(-q, s, x), inv, q);
+__device__ __forceinline__ float quotient(float x, float s, float ninv) {
+  const float nx = -x, q = nx * ninv;
+  return fmaf(fmaf(q, s, nx), ninv, q);
 }
 __device__ __forceinline__ uint2 to_fp8x8(const float (&v)[8], float mul, bool e5m2) {
   uint2 u;
@@ -62,10 +66,10 @@ __device__ __forceinline__ uint2 to_fp8x8(const float (&v)[8], float mul, bool e
   return u;
 }
 // Eight elements of one block.
-__device__ __forceinline__ uint2 quantize8(const float (&v)[8], float s, float inv, bool e5m2) {
+__device__ __forceinline__ uint2 quantize8(const float (&v)[8], float s, float ninv, bool e5m2) {
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s, inv);
+  for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s, ninv);
   return to_fp8x8(q, 1.0f, e5m2);
 }
 

@@ -66,13 +66,13 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
   if (MODE & kRow) {
     // each lane divides for the row that it owns
     const int mine = owned(lane16);
-    const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), inv = __fdiv_rn(1.0f, s), div = divisor(s);
+    const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), ninv = __fdiv_rn(-1.0f, s), div = divisor(s);
     if ((lane16 & 1) == 0 && 16 * mine < rows) p.sr[(r0 + 16 * mine) * p.ldsr + tc] = s;
     unsigned char *q = p.qr + r0 * p.ldqr + c0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int from = (i & 4) * 2 + (i & 2) * 2 + (i & 1) * 2;
-      const float si = __shfl_sync(~0u, div, from, 16), fi = __shfl_sync(~0u, inv, from, 16);
+      const float si = __shfl_sync(~0u, div, from, 16), fi = __shfl_sync(~0u, ninv, from, 16);
       float v[8];
       unpack(raw[i], v);
       if (16 * i < rows) store8_fp8(q + 16 * i * p.ldqr, quantize8(v, si, fi, p.e5m2), n, vec_r);
@@ -88,14 +88,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < 8; ++w) tmax = max_abs(tmax, part[0][w]);
-    const float s = block_scale(tmax, p.e5m2), inv = __fdiv_rn(1.0f, s);
+    const float s = block_scale(tmax, p.e5m2), ninv = __fdiv_rn(-1.0f, s);
     if (threadIdx.x == 0) p.sr[tr * p.ldsr + tc] = s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float v[8];
       unpack(raw[i], v);
       if (16 * i < rows)
-        store8_fp8(p.qr + (r0 + 16 * i) * p.ldqr + c0, quantize8(v, divisor(s), inv, p.e5m2), n, vec_r);
+        store8_fp8(p.qr + (r0 + 16 * i) * p.ldqr + c0, quantize8(v, divisor(s), ninv, p.e5m2), n, vec_r);
     }
   }
   if (MODE & kCol) {
@@ -113,14 +113,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
       const float s = block_scale(a, p.e5m2);
       const int64_t c = tc * 128 + threadIdx.x;
       if (c < p.cols) p.sc[tr * p.ldsc + c] = s;
-      part[0][threadIdx.x] = __fdiv_rn(1.0f, s);
+      part[0][threadIdx.x] = __fdiv_rn(-1.0f, s);
       part[1][threadIdx.x] = divisor(s);
     }
     __syncthreads();
-    float inv[8], scale[8];
+    float ninv[8], scale[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      inv[j] = part[0][lane16 * 8 + j];
+      ninv[j] = part[0][lane16 * 8 + j];
       scale[j] = part[1][lane16 * 8 + j];
     }
 #pragma unroll
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
       float v[8];
       unpack(raw[i], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = quotient(v[j], scale[j], inv[j]);
+      for (int j = 0; j < 8; ++j) v[j] = quotient(v[j], scale[j], ninv[j]);
       if (16 * i < rows)
         store8_fp8(p.qc + (r0 + 16 * i) * p.ldqc + c0, to_fp8x8(v, 1.0f, p.e5m2), n, vec_c);
     }
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(256, 5)
   constexpr int PITCH = 128 + 16 / sizeof(T);   // a 16-byte unit more: rows start in different banks
   extern __shared__ __align__(16) unsigned char tile_smem[];
   T *tile = reinterpret_cast<T *>(tile_smem);
-  __shared__ __align__(16) float part[8][128];   // column maxima of 16 rows, then (part[0]) 1 / scale
+  __shared__ __align__(16) float part[8][128];   // column maxima of 16 rows, then (part[0], part[1]) -1 / scale and scale
   griddep_wait();
   griddep_launch_dependents();
   const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(256, 5)
     for (int j = 0; j < 8; ++j) rmax[i] = max_abs(rmax[i], v[j]);
   }
   const int own = owned(lane16);
-  const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), row_inv = __fdiv_rn(1.0f, s), div = divisor(s);
+  const float s = block_scale(max_of_8x16(rmax, lane16), p.e5m2), row_ninv = __fdiv_rn(-1.0f, s), div = divisor(s);
   if ((lane16 & 1) == 0 && 16 * own < rows) p.sr[(r0 + 16 * own) * p.ldsr + tc] = s;
   __syncthreads();
   if (threadIdx.x < 128) {
@@ -207,27 +207,27 @@ __global__ void __launch_bounds__(256, 5)
     const float t = block_scale(a, p.e5m2);
     const int64_t c = tc * 128 + threadIdx.x;
     if (c < p.cols) p.sc[tr * p.ldsc + c] = t;
-    part[0][threadIdx.x] = __fdiv_rn(1.0f, t);
+    part[0][threadIdx.x] = __fdiv_rn(-1.0f, t);
     part[1][threadIdx.x] = divisor(t);
   }
   __syncthreads();
-  float inv[8], scale[8];
+  float ninv[8], scale[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    inv[j] = part[0][lane16 * 8 + j];
+    ninv[j] = part[0][lane16 * 8 + j];
     scale[j] = part[1][lane16 * 8 + j];
   }
   unsigned char *qr = p.qr + r0 * p.ldqr + c0, *qc = p.qc + r0 * p.ldqc + c0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int from = (i & 4) * 2 + (i & 2) * 2 + (i & 1) * 2;
-    const float si = __shfl_sync(~0u, div, from, 16), fi = __shfl_sync(~0u, row_inv, from, 16);
+    const float si = __shfl_sync(~0u, div, from, 16), fi = __shfl_sync(~0u, row_ninv, from, 16);
     float v[8];
     unpack(load8(mine + 16 * i * PITCH, 8, true), v);
     if (16 * i < rows) {
       store8_fp8(qr + 16 * i * p.ldqr, quantize8(v, si, fi, p.e5m2), n, vec_r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = quotient(v[j], scale[j], inv[j]);
+      for (int j = 0; j < 8; ++j) v[j] = quotient(v[j], scale[j], ninv[j]);
       store8_fp8(qc + 16 * i * p.ldqc, to_fp8x8(v, 1.0f, p.e5m2), n, vec_c);
     }
   }
