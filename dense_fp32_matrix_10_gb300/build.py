@@ -11,10 +11,12 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -52,18 +54,27 @@ def _compile(nvcc, src, obj, log, defines=()):
     return obj
 
 
+def _torch_target(spec) -> str:
+    """What the extension module is built for: torch's version (as its version.py has it) and the interpreter."""
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+        version = re.search(r"__version__\s*=\s*['\"]([^'\"]+)", f.read())
+    return f"torch {version.group(1) if version else '?'}, {sysconfig.get_config_var('SOABI')}"
+
+
 def _torch_extension(force: bool):
-    """Compile csrc/fp8_torch.cpp against the installed torch if it is out of date.  Without torch there is
-    nothing to marshal for."""
+    """Compile csrc/fp8_torch.cpp against the installed torch if it is out of date, or was built for another torch or
+    interpreter.  Without torch there is nothing to marshal for.  The module saves time in fp8.py, which also does
+    without it: where it cannot be built (no compiler, a torch without CUDA) that is a warning."""
     spec = importlib.util.find_spec("torch")
     if spec is None:
         return None
     src, log = os.path.join(CSRC, "fp8_torch.cpp"), os.path.join(BUILD, "fp8_torch.log")
-    torch_dir = os.path.dirname(spec.origin)
-    newest = max([os.path.getmtime(src), os.path.getmtime(os.path.join(torch_dir, "version.py")),
-                  *(os.path.getmtime(h) for h in glob.glob(os.path.join(INCLUDE, "*.h")))])
-    if not force and os.path.exists(TORCH_EXT) and os.path.getmtime(TORCH_EXT) >= newest:
-        return TORCH_EXT
+    torch_dir, target, stamp = os.path.dirname(spec.origin), _torch_target(spec), os.path.join(BUILD, "fp8_torch.target")
+    newest = max([os.path.getmtime(src), *(os.path.getmtime(h) for h in glob.glob(os.path.join(INCLUDE, "*.h")))])
+    if not force and os.path.exists(TORCH_EXT) and os.path.getmtime(TORCH_EXT) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == target:
+                return TORCH_EXT
     cuda_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     tmp = TORCH_EXT + ".tmp.%d" % os.getpid()
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -71,12 +82,22 @@ def _torch_extension(force: bool):
            "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-isystem", cuda_include, src, "-o", tmp,
            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
-    proc = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        proc = subprocess.run(cmd, capture_output=True, text=True)
+        failed, said = proc.returncode != 0, proc.stdout + proc.stderr
+    except OSError as e:
+        failed, said = True, str(e)
     with open(log, "w") as f:
-        f.write(" ".join(cmd) + "\n" + proc.stdout + proc.stderr)
-    if proc.returncode != 0:
-        raise RuntimeError("g++ failed on fp8_torch.cpp:\n" + proc.stderr[-4000:])
+        f.write(" ".join(cmd) + "\n" + said)
+    if failed:
+        if os.path.exists(TORCH_EXT):   # of another torch, or of other entry points
+            os.remove(TORCH_EXT)
+        warnings.warn(f"the extension module of fp8.py was not built (see {log}); its calls take some 8 us longer:\n"
+                      + said[-1000:])
+        return None
     os.replace(tmp, TORCH_EXT)
+    with open(stamp, "w") as f:
+        f.write(target)
     return TORCH_EXT
 
 
@@ -108,8 +129,6 @@ def build(force: bool = False, jobs: int = None, verbose: bool = False, defines=
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         extension = None if out else ex.submit(_torch_extension, force)
         list(ex.map(lambda t: _compile(nvcc, *t, defines=defines), todo))
-        if extension is not None:
-            extension.result()
     relink = force or bool(todo) or not os.path.exists(lib) or \
         os.path.getmtime(lib) < max(os.path.getmtime(o) for o in objs)
     if relink:
@@ -119,6 +138,8 @@ def build(force: bool = False, jobs: int = None, verbose: bool = False, defines=
         if proc.returncode != 0:
             raise RuntimeError("link failed:\n" + proc.stderr[-4000:])
         os.replace(tmp, lib)
+    if extension is not None:
+        extension.result()
     if verbose:
         for _, obj, log in todo:
             sys.stdout.write(open(log).read())
