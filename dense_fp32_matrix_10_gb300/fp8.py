@@ -173,6 +173,8 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 def _on(stream, dev):
     """The context in which a call allocates and runs, or None if that is the current one."""
     if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"stream is of cuda:{stream.device.index}, the tensors are on cuda:{dev}")
         return torch.cuda.stream(stream)
     return None if dev == _current_device() else torch.cuda.device(dev)
 
