@@ -34,8 +34,8 @@ from ._binding import (  # noqa: F401
 
 _FP8_NAMES = (
     "RmsNormFp8", "gemm_fp8", "quantize_fp8", "quantize_fp8_both", "rms_norm_backward", "rms_norm_fp8", "sgemm_fp8",
-    "sgemm_fp8_quantize", "sgemm_fp8_quantize_both", "sgemm_rms_norm_backward", "sgemm_rms_norm_backward_workspace",
-    "sgemm_rms_norm_fp8")
+    "sgemm_fp8_quantize", "sgemm_fp8_quantize_both", "sgemm_fp8_select_form", "sgemm_rms_norm_backward",
+    "sgemm_rms_norm_backward_workspace", "sgemm_rms_norm_fp8")
 
 
 def __getattr__(name):

@@ -32,6 +32,12 @@ struct Fp8Params {
   int *status;
 };
 
+// The form of the kernel for a product, and the CTAs that share a tile's blocks of k (fp8_tc.cu).
+struct Fp8Choice {
+  sgemm_fp8_form_t form;
+  int split;
+};
+Fp8Choice choose_fp8_form(const Fp8Params &p, int sm_count);
 // The product on the tensor cores, any layout (fp8_tc.cu).
 cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s);
 // C = beta * C (fp8_scale_c.cu).

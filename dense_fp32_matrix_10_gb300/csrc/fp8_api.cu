@@ -125,6 +125,30 @@ sgemm_status_t sgemm_fp8(int transA, int transB, int64_t M, int64_t N, int64_t K
   return queued(launch_fp8_product(p, d->sm_count, s), 1);
 }
 
+int sgemm_fp8_select_form(int transA, int transB, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
+                          const void *B, int64_t ldb, int blockB, float beta, const void *C, sgemm_type_t typeC,
+                          int64_t ldc, int *split) {
+  const int ta = norm_op(transA), tb = norm_op(transB);
+  if (ta < 0 || tb < 0 || !good_dim(M) || !good_dim(N) || !good_dim(K) || M == 0 || N == 0 || K == 0) return -1;
+  if (!is_float_type(typeC) || (blockB != 1 && blockB != 128)) return -1;
+  if (!good_ld(lda, ta ? M : K) || !good_ld(ldb, tb ? K : N) || !good_ld(ldc, N)) return -1;
+  Fp8Params p = {};
+  p.a = {static_cast<const unsigned char *>(A), nullptr, lda, 0, 0, ta == 1, 0};
+  p.b = {static_cast<const unsigned char *>(B), nullptr, ldb, 0, 0, tb == 0, blockB == 128 ? 7 : 0};
+  p.C = const_cast<void *>(C);
+  p.ldc = ldc;
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.typeC = typeC;
+  p.beta = beta;
+  sgemm_status_t why = SGEMM_SUCCESS;
+  const DeviceState *d = device_state(&why);
+  const Fp8Choice c = choose_fp8_form(p, d ? d->sm_count : 152);
+  if (split) *split = c.split;
+  return c.form;
+}
+
 sgemm_status_t sgemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, sgemm_type_t typeX, int64_t ldx, void *Q,
                                   sgemm_type_t typeQ, int64_t ldq, float *S, int64_t lds, int block_rows,
                                   int block_cols, void *stream) {

@@ -191,7 +191,7 @@ int pick_split(int64_t kblocks, int most, F cycles) {
 
 }  // namespace
 
-cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s) {
+Fp8Choice choose_fp8_form(const Fp8Params &p, int sm_count) {
   const int64_t kb = cdiv64(p.K, 128), slots = 2 * sm_count;
   const bool readable =
       tma_readable(p.a, p.a.inner_rows ? p.K : p.M) && tma_readable(p.b, p.b.inner_rows ? p.K : p.N);
@@ -199,8 +199,7 @@ cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s)
     const int cols = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
     const int split =
         pick_split(kb, 8, [&](int n) { return few_cycles(cdiv64(p.N, 128), kb, cols, n, sm_count); });
-    if (cols == 16) return launch<Few16>(p, split, s);
-    return cols == 32 ? launch<Few32>(p, split, s) : launch<Few64>(p, split, s);
+    return {cols == 16 ? SGEMM_FP8_FORM_FEW_16 : cols == 32 ? SGEMM_FP8_FORM_FEW_32 : SGEMM_FP8_FORM_FEW_64, split};
   }
   const bool vec = p.b.shift == 0, aligned = aligned_rows(p.C, p.ldc, size_of(p.typeC), 16);
   const int64_t rows = cdiv64(p.M, 128);
@@ -211,7 +210,7 @@ cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s)
     const int n = pick_split(kb, 4, [&](int n) {
       return tile_cycles(rows * cdiv64(p.N, 128), 3 * kb, 128, n, sm_count, false, aligned);
     });
-    return vec ? launch<LoadedVec>(p, n, s) : launch<Loaded>(p, n, s);
+    return {SGEMM_FP8_FORM_LOADED, n};
   }
   const int split = pick_split(kb, 4, tiles), split_half = pick_split(kb, 4, halves);
   const int64_t tile = tiles(split), half = halves(split_half);
@@ -223,12 +222,28 @@ cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s)
     // (a TMA store writes whole 16 bytes at the end of a row)
     const int size = size_of(p.typeC);
     const bool bulk = aligned && p.beta == 0.0f && static_cast<int64_t>(p.N) * size % 16 == 0 && p.ldc < kMaxLd / size;
-    if (vec) return bulk ? launch<PairVecBulk>(p, 1, s) : launch<PairVec>(p, 1, s);
-    if (bulk) return launch<PairBulk>(p, 1, s);
-    return aligned ? launch<Pair>(p, 1, s) : launch<PairStaged>(p, 1, s);
+    if (bulk) return {SGEMM_FP8_FORM_PAIR_BULK, 1};
+    return {aligned || vec ? SGEMM_FP8_FORM_PAIR : SGEMM_FP8_FORM_PAIR_STAGED, 1};
   }
-  if (half < tile) return vec ? launch<HalfVec>(p, split_half, s) : launch<Half>(p, split_half, s);
-  return vec ? launch<TileVec>(p, split, s) : launch<Tile>(p, split, s);
+  if (half < tile) return {SGEMM_FP8_FORM_HALF, split_half};
+  return {SGEMM_FP8_FORM_TILE, split};
+}
+
+cudaError_t launch_fp8_product(const Fp8Params &p, int sm_count, cudaStream_t s) {
+  const Fp8Choice c = choose_fp8_form(p, sm_count);
+  const bool vec = p.b.shift == 0;
+  switch (c.form) {
+    case SGEMM_FP8_FORM_FEW_16: return launch<Few16>(p, c.split, s);
+    case SGEMM_FP8_FORM_FEW_32: return launch<Few32>(p, c.split, s);
+    case SGEMM_FP8_FORM_FEW_64: return launch<Few64>(p, c.split, s);
+    case SGEMM_FP8_FORM_HALF: return vec ? launch<HalfVec>(p, c.split, s) : launch<Half>(p, c.split, s);
+    case SGEMM_FP8_FORM_TILE: return vec ? launch<TileVec>(p, c.split, s) : launch<Tile>(p, c.split, s);
+    case SGEMM_FP8_FORM_LOADED: return vec ? launch<LoadedVec>(p, c.split, s) : launch<Loaded>(p, c.split, s);
+    case SGEMM_FP8_FORM_PAIR: return vec ? launch<PairVec>(p, 1, s) : launch<Pair>(p, 1, s);
+    case SGEMM_FP8_FORM_PAIR_STAGED: return launch<PairStaged>(p, 1, s);
+    case SGEMM_FP8_FORM_PAIR_BULK: return vec ? launch<PairVecBulk>(p, 1, s) : launch<PairBulk>(p, 1, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace sg

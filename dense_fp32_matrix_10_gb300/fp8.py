@@ -62,6 +62,9 @@ def _library():
         for f in (lib.sgemm_fp8, lib.sgemm_fp8_quantize, lib.sgemm_fp8_quantize_both, lib.sgemm_rms_norm_fp8,
                   lib.sgemm_rms_norm_backward):
             f.restype = _INT
+        lib.sgemm_fp8_select_form.argtypes = [_INT, _INT, _I64, _I64, _I64, _VP, _I64, _VP, _I64, _INT, _F, _VP, _INT,
+                                              _I64, ctypes.POINTER(_INT)]
+        lib.sgemm_fp8_select_form.restype = _INT
         lib.sgemm_rms_norm_backward_workspace.argtypes = [_I64, _I64]
         lib.sgemm_rms_norm_backward_workspace.restype = ctypes.c_size_t
         global _usual
@@ -90,6 +93,17 @@ def sgemm_fp8(transA, transB, M, N, K, alpha, A, typeA, lda, SA, ldsa, blockA, B
     """C = alpha*op(A)*op(B) + beta*C with block-scaled 8-bit A and B."""
     _raise("sgemm_fp8", _library().sgemm_fp8(_op(transA), _op(transB), M, N, K, alpha, A, typeA, lda, SA, ldsa, blockA,
                                              B, typeB, ldb, SB, ldsb, blockB, beta, C, typeC, ldc, stream))
+
+
+FP8_FORMS = ("few_16", "few_32", "few_64", "half", "tile", "loaded", "pair", "pair_staged", "pair_bulk")
+
+
+def sgemm_fp8_select_form(transA, transB, M, N, K, A, lda, B, ldb, blockB, beta, C, typeC, ldc):
+    """(name of the form, CTAs sharing a tile) that sgemm_fp8 would run, or None if it would multiply nothing."""
+    split = _INT(0)
+    form = _library().sgemm_fp8_select_form(_op(transA), _op(transB), M, N, K, A, lda, B, ldb, blockB, beta, C, typeC,
+                                            ldc, ctypes.byref(split))
+    return None if form < 0 else (FP8_FORMS[form], split.value)
 
 
 def sgemm_fp8_quantize(rows, cols, X, typeX, ldx, Q, typeQ, ldq, S, lds, block_rows, block_cols, stream=None):

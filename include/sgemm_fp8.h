@@ -72,6 +72,30 @@ SGEMM_API sgemm_status_t sgemm_fp8(int transA, int transB, int64_t M, int64_t N,
                                    int blockB, float beta, void *C, sgemm_type_t typeC, int64_t ldc,
                                    void *stream);
 
+/* The forms of sgemm_fp8()'s kernel. */
+typedef enum sgemm_fp8_form {
+  SGEMM_FP8_FORM_FEW_16 = 0, /* up to 16 rows of C: 128 of its columns x 16 rows, one CTA or a cluster */
+  SGEMM_FP8_FORM_FEW_32 = 1, /* up to 32 */
+  SGEMM_FP8_FORM_FEW_64 = 2, /* up to 64 */
+  SGEMM_FP8_FORM_HALF = 3,   /* 128 x 64, one CTA or a cluster */
+  SGEMM_FP8_FORM_TILE = 4,   /* 128 x 128, one CTA or a cluster */
+  SGEMM_FP8_FORM_LOADED = 5, /* the same, of operands that TMA cannot read */
+  SGEMM_FP8_FORM_PAIR = 6,   /* 256 x 256 on two SMs, C written by the threads */
+  SGEMM_FP8_FORM_PAIR_STAGED = 7, /* the same for rows of C off 16 bytes, through shared memory */
+  SGEMM_FP8_FORM_PAIR_BULK = 8    /* the same with TMA stores */
+} sgemm_fp8_form_t;
+
+/*
+ * The form that sgemm_fp8() would run for these arguments, or -1 if they are
+ * invalid or nothing is multiplied; *split (if not NULL) is the number of CTAs
+ * of a cluster that share the inner dimension of one tile.  Host only, as
+ * sgemm_select_algo(); without a usable device, for 152 SMs.
+ */
+SGEMM_API int sgemm_fp8_select_form(int transA, int transB, int64_t M, int64_t N, int64_t K,
+                                    const void *A, int64_t lda, const void *B, int64_t ldb,
+                                    int blockB, float beta, const void *C, sgemm_type_t typeC,
+                                    int64_t ldc, int *split);
+
 /*
  * Quantises X (rows x cols; F32, BF16 or F16) in blocks of block_rows x
  * block_cols, which are 1 x 128, 128 x 1 or 128 x 128: with a the largest |x|
