@@ -11,6 +11,11 @@
 // truncating accumulator never holds more than 128 products and every scale is
 // applied in FP32.
 //
+// The two scales of a block are multiplied before its sum is there, one multiplication for 128 columns (or, VEC, one
+// a value beside the tensor memory's loads).  Their product may leave FP32's normal range where the scaled sum does
+// not; the interface states what that costs.  Scaling the sum twice would be a second multiplication for every value
+// in all forms, and a test for the rare case would take its slow way at every padded row (least scale).
+//
 // The tile's rows (tensor memory lanes, one per thread) come from the operand
 // `row`, its columns from `col`.  A row's scale is one value per thread and block;
 // a column's scale is one value for 128 columns, or one each (VEC).

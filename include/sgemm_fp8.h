@@ -21,7 +21,8 @@
  * results.
  *
  * Arithmetic is FP32 throughout: every sum, norm and scale is held in 32 bits,
- * and a result is rounded once, where it is stored.  Subnormals are kept.
+ * and a result is rounded once, where it is stored.  Subnormals are kept (of the
+ * product of two scales, as FP32 holds them: see sgemm_fp8()).
  */
 #ifndef DENSE_FP32_MATRIX_10_GB300_SGEMM_FP8_H_
 #define DENSE_FP32_MATRIX_10_GB300_SGEMM_FP8_H_
@@ -61,7 +62,12 @@ typedef enum sgemm_type {
  * T,N with blocks 1 and 1.
  *
  * Each block's products are summed on the tensor cores, then scaled and added
- * to the output's sum in FP32 registers.  Degenerate cases as in sgemm():
+ * to the output's sum in FP32 registers.  The two scales of a block are
+ * multiplied first, in FP32: where SA * SB is a normal number (2^-126 to
+ * 2^128) the block counts in full.  Below, its part of C is off by up to
+ * 2^-150 times its unscaled sum of magnitudes (2^-125 in all for E4M3 by E4M3,
+ * 2^-111 for E5M2 by E5M2; a block of zeros still counts nothing); from 2^128
+ * on it is an infinity, or NaN where the block's sum is zero.  Degenerate cases as in sgemm():
  * K == 0 or alpha == 0 give C = beta * C without reading A, B or the scales,
  * and beta == 0 never reads C.  One launch; deterministic.
  */
