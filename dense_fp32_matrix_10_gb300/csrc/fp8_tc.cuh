@@ -35,7 +35,7 @@
 // columns is handed to the epilogue and back while the only other one is filled, about 450 ns a
 // block of k, where the MMAs alone take 320; and the 1400 W of the card, reached in sustained runs of
 // 8192^3 (2.5 PFLOP/s, 448 us; 401 in short ones).  Tried, at 4096 x 4096 x 16384 in 245 us then: four
-// accumulators of 128 columns (345; such an MMA takes nearly as long as one of 256), sixteen epilogue
+// accumulators of 128 columns (345), sixteen epilogue
 // warps of 64 columns (285), the row scales through shared memory (279), four at a time (258).
 // Single CTAs (128 x 128 or 128 x 64, two an SM) are bound the same way (512 x 4096 x 8192 25.2 us, without
 // any copies 22.8), the few-token forms by their weights' way from memory and by latencies.

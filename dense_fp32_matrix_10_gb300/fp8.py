@@ -19,7 +19,8 @@ belongs to that stream) or on torch's current stream, and returns once its work
 is queued.  Nothing here computes; there is no CPU fallback.  The usual calls
 (plain tensors of the current device, its current stream) are marshalled by the
 extension module _fp8_torch where it has been built; it hands back what it does
-not take, and the code here checks everything and says what is wrong.
+not take, and the code here checks everything and says what is wrong.  Its outputs come straight from the caching
+allocator: dispatch modes and torch.utils.deterministic's filling do not see them.
 """
 import collections
 import ctypes
@@ -330,8 +331,8 @@ def rms_norm_fp8(x, weight, residual=None, eps=1e-6, dtype=torch.float8_e4m3fn, 
     """RMS norm of x + residual, quantised in (1, 128) blocks: RmsNormFp8(q, scale, h, y, rstd).
 
     h = x + residual in x's type (None without a residual: h is x).  With training=True also y, the norm in x's
-    type, and rstd = 1 / sqrt(mean(h^2) + eps) per row, which rms_norm_backward wants.  `weight` is float32 or of
-    x's type."""
+    type, and rstd = 1 / sqrt(mean(h^2) + eps) per row, which rms_norm_backward wants (not set for rows without
+    elements).  `weight` is float32 or of x's type."""
     if _usual is not None and stream is None and dtype in _FP8:
         r = _usual.norm(x, weight, residual, eps, _FP8[dtype], training)
         if r is not None:

@@ -133,7 +133,9 @@ SGEMM_API sgemm_status_t sgemm_fp8_quantize_both(int64_t rows, int64_t cols, con
  * RMS norm of x + r with an 8-bit output, row by row:
  *
  *   h = x + r,   t = 1 / sqrt(mean(h^2) + eps),   y = h * t * w,
- *   (q, s) = y quantised in 1 x 128 blocks (sgemm_fp8_quantize; q = y * (1 / s) here)
+ *   (q, s) = y quantised in 1 x 128 blocks (as sgemm_fp8_quantize(), but q is
+ *            y * (1 / s) rounded: beside a middle of two 8-bit values, within
+ *            2^-22 of it, that may be the other neighbour than for y / s)
  *
  * X and R (NULL: h = x) are rows x cols of typeX (F32, BF16, F16), W has cols
  * elements of typeW (F32 or typeX).  Q and S are always written; H and Y (of
