@@ -21,6 +21,10 @@ High level (torch tensors): ``gemm``, ``gemm_strided_batched``, ``transpose``.
 The linear layer in 8-bit floating point (module ``fp8``, ``include/sgemm_fp8.h``):
 ``gemm_fp8``, ``quantize_fp8``, ``quantize_fp8_both``, ``rms_norm_fp8``,
 ``rms_norm_backward`` on torch tensors, and the ``sgemm_*`` functions they call.
+
+Around a gated block's products (module ``fp8_block``, ``include/sgemm_fp8_block.h``):
+``sandwich_norm_fp8``, ``sandwich_norm_backward``, ``swiglu_fp8``, ``swiglu_backward_fp8``,
+``requantize_fp8``, and the ``sgemm_*`` functions they call.
 """
 from ._binding import (  # noqa: F401
     ALGO_AUTO, ALGO_NAIVE, ALGO_REG_2X2, ALGO_REG_4X4, ALGO_SIMT_CPASYNC, ALGO_SIMT_TMA,
@@ -36,16 +40,24 @@ _FP8_NAMES = (
     "RmsNormFp8", "gemm_fp8", "quantize_fp8", "quantize_fp8_both", "rms_norm_backward", "rms_norm_fp8", "sgemm_fp8",
     "sgemm_fp8_quantize", "sgemm_fp8_quantize_both", "sgemm_fp8_select_form", "sgemm_rms_norm_backward",
     "sgemm_rms_norm_backward_workspace", "sgemm_rms_norm_fp8")
+_FP8_BLOCK_NAMES = (
+    "SandwichNormFp8", "SandwichNormGrad", "SwigluFp8", "SwigluGradFp8", "requantize_fp8", "sandwich_norm_backward",
+    "sandwich_norm_fp8", "swiglu_backward_fp8", "swiglu_fp8", "sgemm_fp8_requantize", "sgemm_sandwich_norm_backward",
+    "sgemm_sandwich_norm_backward_workspace", "sgemm_sandwich_norm_fp8", "sgemm_swiglu_backward_fp8", "sgemm_swiglu_fp8")
 
 
 def __getattr__(name):
-    """The names of module fp8, which imports torch, on first use."""
+    """The names of modules fp8 and fp8_block, which import torch, on first use."""
     if name in _FP8_NAMES:
         from . import fp8
         globals().update((n, getattr(fp8, n)) for n in _FP8_NAMES)
+        return globals()[name]
+    if name in _FP8_BLOCK_NAMES:
+        from . import fp8_block
+        globals().update((n, getattr(fp8_block, n)) for n in _FP8_BLOCK_NAMES)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted({*globals(), *_FP8_NAMES})
+    return sorted({*globals(), *_FP8_NAMES, *_FP8_BLOCK_NAMES})

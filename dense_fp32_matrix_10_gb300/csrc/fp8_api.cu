@@ -4,58 +4,10 @@
 
 #include "dispatch.h"
 #include "fp8.h"
+#include "fp8_checks.h"
 
 namespace sg {
 namespace {
-
-using u128 = unsigned __int128;
-
-bool is_float_type(int t) { return t == SGEMM_TYPE_F32 || t == SGEMM_TYPE_BF16 || t == SGEMM_TYPE_F16; }
-bool is_fp8_type(int t) { return t == SGEMM_TYPE_E4M3 || t == SGEMM_TYPE_E5M2; }
-int type_size(int t) { return t == SGEMM_TYPE_F32 ? 4 : is_fp8_type(t) ? 1 : 2; }
-
-bool good_dim(int64_t v) { return v >= 0 && v <= kMaxDim; }
-bool good_ld(int64_t ld, int64_t cols) { return ld >= (cols > 1 ? cols : 1) && ld <= kMaxLd; }
-
-// A matrix that a call reads or writes.
-struct Range {
-  const void *p;
-  int64_t rows, cols, ld;
-  int elem;
-  bool output;
-};
-
-// Present, inside the address space, elements on their own alignment, outputs
-// apart from everything else.  A range of null pointer and no rows stands for
-// an argument that was not given.
-sgemm_status_t check_ranges(const Range *r, int n) {
-  u128 lo[12], hi[12];
-  for (int i = 0; i < n; ++i) {
-    lo[i] = hi[i] = 0;
-    if (r[i].rows == 0 || r[i].cols == 0) continue;
-    if (!r[i].p) return SGEMM_ERR_INVALID_VALUE;
-    lo[i] = reinterpret_cast<uintptr_t>(r[i].p);
-    if (lo[i] % r[i].elem != 0) return SGEMM_ERR_INVALID_VALUE;
-    hi[i] = lo[i] + static_cast<u128>(r[i].elem) *
-                        (static_cast<u128>(r[i].rows - 1) * static_cast<u128>(r[i].ld) + static_cast<u128>(r[i].cols));
-    if (hi[i] > static_cast<u128>(1) << 64) return SGEMM_ERR_INVALID_VALUE;
-  }
-  for (int i = 0; i < n; ++i)
-    for (int j = 0; j < n; ++j)
-      if (i != j && r[i].output && lo[i] < hi[j] && lo[j] < hi[i]) return SGEMM_ERR_ALIASING;
-  return SGEMM_SUCCESS;
-}
-
-sgemm_status_t queued(cudaError_t e, int launches) {
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return SGEMM_ERR_LAUNCH;
-  }
-  t_last_launches = launches;
-  return SGEMM_SUCCESS;
-}
-
-int64_t blocks_of(int64_t n, int block) { return (n + block - 1) / block; }
 
 sgemm_status_t quantize(const QuantizeParams &p, int br, int bc, bool both, cudaStream_t stream) {
   const int e = type_size(p.typeX);
@@ -65,7 +17,7 @@ sgemm_status_t quantize(const QuantizeParams &p, int br, int bc, bool both, cuda
       {p.sr, both || p.qr ? blocks_of(p.rows, both ? 1 : br) : 0, blocks_of(p.cols, both ? 128 : bc), p.ldsr, 4, true},
       {p.qc, both || p.qc ? p.rows : 0, p.cols, p.ldqc, 1, true},
       {p.sc, both || p.qc ? blocks_of(p.rows, 128) : 0, p.cols, p.ldsc, 4, true}};
-  const sgemm_status_t st = check_ranges(r, 5);
+  const sgemm_status_t st = check_ranges(r);
   if (st != SGEMM_SUCCESS) return st;
   sgemm_status_t why = SGEMM_SUCCESS;
   if (!device_state(&why)) return why;
@@ -102,7 +54,7 @@ sgemm_status_t sgemm_fp8(int transA, int transB, int64_t M, int64_t N, int64_t K
                       {SA, has * (ta ? kb : ma), ta ? ma : kb, ldsa, 4, false},
                       {B, has * (tb ? N : K), tb ? K : N, ldb, 1, false},
                       {SB, has * (tb ? nb : kb), tb ? kb : nb, ldsb, 4, false}};
-  const sgemm_status_t st = check_ranges(r, 5);
+  const sgemm_status_t st = check_ranges(r);
   if (st != SGEMM_SUCCESS) return st;
   sgemm_status_t why = SGEMM_SUCCESS;
   DeviceState *d = device_state(&why);
@@ -227,7 +179,7 @@ sgemm_status_t sgemm_rms_norm_fp8(int64_t rows, int64_t cols, float eps, const v
                       {H, H ? rows : 0, cols, ldh, e, true}, {Y, Y ? rows : 0, cols, ldy, e, true},
                       {Q, rows, cols, ldq, 1, true},       {S, rows, kb, lds, 4, true},
                       {T, T ? 1 : 0, rows, rows, 4, true}};
-  const sgemm_status_t st = check_ranges(r, 8);
+  const sgemm_status_t st = check_ranges(r);
   if (st != SGEMM_SUCCESS) return st;
   sgemm_status_t why = SGEMM_SUCCESS;
   DeviceState *d = device_state(&why);
@@ -285,7 +237,7 @@ sgemm_status_t sgemm_rms_norm_backward(int64_t rows, int64_t cols, const void *D
                       {DX, rows, cols, lddx, e, true},
                       {DW, DW ? 1 : 0, cols, cols, type_size(typeW), true},
                       {workspace, need ? 1 : 0, static_cast<int64_t>(need / 4), static_cast<int64_t>(need / 4), 4, true}};
-  const sgemm_status_t st = check_ranges(r, 8);
+  const sgemm_status_t st = check_ranges(r);
   if (st != SGEMM_SUCCESS) return st;
   sgemm_status_t why = SGEMM_SUCCESS;
   if (!device_state(&why)) return why;
