@@ -1,8 +1,8 @@
-// fp8_torch.cpp -- Python extension module that marshals the usual calls of fp8.py: plain tensors of one
-// device, the current one, on its current stream.  It checks what those need, allocates the outputs and calls
-// the C ABI; for anything else (another layout, a mistake, an error) it returns None, and fp8.py, which
-// handles every case, goes on.  It computes nothing: it only takes some 8 of 13 us off a call's way through
-// Python.
+// fp8_torch.cpp -- Python extension module that marshals the usual calls of fp8.py and fp8_block.py: plain
+// tensors of one device, the current one, on its current stream.  It checks what those need, allocates the
+// outputs and calls the C ABI; for anything else (another layout, a mistake, an error) it returns None, and the
+// Python code, which handles every case, goes on.  It computes nothing: it only takes some 8 of 13 us off a
+// call's way through Python (more where a call has many arguments).
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
@@ -10,7 +10,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
-#include "sgemm_fp8.h"
+#include "sgemm_fp8_block.h"
 
 namespace {
 
@@ -20,6 +20,12 @@ decltype(&sgemm_fp8_quantize_both) f_quantize_both;
 decltype(&sgemm_rms_norm_fp8) f_norm;
 decltype(&sgemm_rms_norm_backward) f_norm_backward;
 decltype(&sgemm_rms_norm_backward_workspace) f_workspace;
+decltype(&sgemm_sandwich_norm_fp8) f_sandwich;
+decltype(&sgemm_sandwich_norm_backward) f_sandwich_backward;
+decltype(&sgemm_sandwich_norm_backward_workspace) f_sandwich_workspace;
+decltype(&sgemm_swiglu_fp8) f_swiglu;
+decltype(&sgemm_swiglu_backward_fp8) f_swiglu_backward;
+decltype(&sgemm_fp8_requantize) f_requantize;
 
 int float_type(at::ScalarType t) {
   switch (t) {
@@ -249,14 +255,220 @@ PyObject *norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------------ around a gated block's products
+sgemm_type_t type_code(at::ScalarType t) {
+  const int f = float_type(t);
+  return static_cast<sgemm_type_t>(f >= 0 ? f : fp8_type(t));
+}
+bool fits(const Matrix &m, int64_t rows, int64_t cols, int dev) { return m.rows == rows && m.cols == cols && m.dev == dev; }
+
+// A matrix of the call's type, or its checkpoint: a pair (q, scale).
+struct KeptMatrix {
+  Matrix m, s;
+  bool set(PyObject *o, const Matrix &like) {
+    if (!PyTuple_CheckExact(o)) return m.set(o) && m.type == like.type && fits(m, like.rows, like.cols, like.dev);
+    return PyTuple_GET_SIZE(o) == 2 && m.set(PyTuple_GET_ITEM(o, 0)) && s.set(PyTuple_GET_ITEM(o, 1)) &&
+           fp8_type(m.type) >= 0 && s.type == at::kFloat && fits(m, like.rows, like.cols, like.dev) &&
+           fits(s, like.rows, blocks(like.cols), like.dev);
+  }
+  const float *scales() const { return static_cast<const float *>(s.p); }
+};
+
+// A gate: none, a vector for all rows, or a matrix with one row for each of as many runs of rows.
+struct GateRows {
+  const at::Tensor *t = nullptr;
+  void *p = nullptr;
+  int64_t ld = 1, group = 1;
+  sgemm_type_t type = SGEMM_TYPE_F32;
+  bool set(PyObject *o, const Matrix &x) {
+    if (o == Py_None) return true;
+    if (!THPVariable_CheckExact(o)) return false;
+    Matrix m;
+    if (THPVariable_Unpack(o).dim() == 1) {
+      if (!vector(o, x.cols, x.dev, t)) return false;
+      ld = at_least_1(x.cols);
+      group = at_least_1(x.rows);
+    } else {
+      if (!m.set(o) || m.cols != x.cols || m.dev != x.dev || m.rows < 1 || x.rows % m.rows != 0) return false;
+      t = m.t;
+      ld = m.ld;
+      group = at_least_1(x.rows / m.rows);
+    }
+    p = t->data_ptr();
+    const int f = float_type(t->scalar_type());
+    type = static_cast<sgemm_type_t>(f);
+    return f >= 0 && (f == SGEMM_TYPE_F32 || t->scalar_type() == x.type);
+  }
+};
+
+// The two weights of the norms around a block.
+struct Weights {
+  const at::Tensor *post = nullptr, *pre = nullptr;
+  sgemm_type_t type = SGEMM_TYPE_F32;
+  bool set(PyObject *a, PyObject *b, const Matrix &x) {
+    if (!vector(a, x.cols, x.dev, post) || !vector(b, x.cols, x.dev, pre)) return false;
+    const int f = float_type(pre->scalar_type());
+    type = static_cast<sgemm_type_t>(f);
+    return post->scalar_type() == pre->scalar_type() && f >= 0 && (f == SGEMM_TYPE_F32 || pre->scalar_type() == x.type);
+  }
+};
+
+// The checkpoints of two rows x cols matrices (not allocated for type < 0).
+struct Checkpoints {
+  at::Tensor q[2], s[2];
+  int64_t ld = 1, lds = 1;
+  void make(const Matrix &like, int type) {
+    if (type < 0) return;
+    lds = at_least_1(blocks(like.cols));
+    for (int i = 0; i < 2; ++i) {
+      q[i] = empty_fp8(like.rows, like.cols, like, fp8_scalar(type), ld);
+      s[i] = empty({like.rows, blocks(like.cols)}, like, at::kFloat);
+    }
+  }
+  void *qp(int i) const { return q[i].defined() ? q[i].data_ptr() : nullptr; }
+  float *sp(int i) const { return s[i].defined() ? s[i].data_ptr<float>() : nullptr; }
+  PyObject *pair(int i) {
+    if (!q[i].defined()) Py_RETURN_NONE;
+    return Py_BuildValue("(NN)", wrap(std::move(q[i])), wrap(std::move(s[i])));
+  }
+};
+
+// (a, x, post_weight, weight, gate or None, residual_scale, eps, 8-bit type, training, the checkpoints' 8-bit type or -1)
+// -> (q, scale, h, post_rstd, rstd, a8, h8)
+PyObject *sandwich_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    Matrix x, r;
+    Weights w;
+    GateRows gate;
+    USUAL(n == 10 && x.set(a[0]) && r.set(a[1]) && float_type(x.type) >= 0 && r.type == x.type &&
+          fits(r, x.rows, x.cols, x.dev) && w.set(a[2], a[3], x) && gate.set(a[4], x) && current(x.dev));
+    const double rho = PyFloat_AsDouble(a[5]), eps = PyFloat_AsDouble(a[6]);
+    const int tq = static_cast<int>(PyLong_AsLong(a[7])), training = PyObject_IsTrue(a[8]);
+    const int tk = static_cast<int>(PyLong_AsLong(a[9]));
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+    const int64_t kb = blocks(x.cols), ld = at_least_1(x.cols);
+    int64_t ldq;
+    at::Tensor q = empty_fp8(x.rows, x.cols, x, fp8_scalar(tq), ldq), s = empty({x.rows, kb}, x, at::kFloat);
+    at::Tensor h = empty({x.rows, x.cols}, x, x.type), tp, t;
+    if (training) {
+      tp = empty({x.rows}, x, at::kFloat);
+      t = empty({x.rows}, x, at::kFloat);
+    }
+    Checkpoints k;
+    k.make(x, tk);
+    USUAL(queue(f_sandwich, x.rows, x.cols, static_cast<float>(eps), static_cast<float>(rho), x.p, x.ld, r.p, r.ld,
+                type_code(x.type), w.post->data_ptr(), w.pre->data_ptr(), w.type, gate.p, gate.ld, gate.type, gate.group,
+                h.data_ptr(), ld, q.data_ptr(), static_cast<sgemm_type_t>(tq), ldq, s.data_ptr<float>(), at_least_1(kb),
+                training ? tp.data_ptr<float>() : nullptr, training ? t.data_ptr<float>() : nullptr, k.qp(0), k.ld, k.sp(0),
+                k.lds, k.qp(1), k.ld, k.sp(1), k.lds, static_cast<sgemm_type_t>(tk), stream_of(x.dev)) == SGEMM_SUCCESS);
+    return Py_BuildValue("(NNNNNNN)", wrap(std::move(q)), wrap(std::move(s)), wrap(std::move(h)),
+                         wrap_or_none(std::move(tp)), wrap_or_none(std::move(t)), k.pair(0), k.pair(1));
+  });
+}
+
+// (dy, a, h, post_weight, weight, post_rstd, rstd, gate or None, residual_scale, dh or None)
+// -> (da, dx, dpost_weight, dweight, dgate)
+PyObject *sandwich_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    Matrix dy, dh;
+    KeptMatrix A, H;
+    Weights w;
+    GateRows gate;
+    const at::Tensor *tp, *t;
+    USUAL(n == 10 && dy.set(a[0]) && float_type(dy.type) >= 0 && A.set(a[1], dy) && H.set(a[2], dy) && w.set(a[3], a[4], dy) &&
+          vector(a[5], dy.rows, dy.dev, tp) && vector(a[6], dy.rows, dy.dev, t) && gate.set(a[7], dy) && current(dy.dev));
+    USUAL(tp->scalar_type() == at::kFloat && t->scalar_type() == at::kFloat && dy.rows > 0);
+    const double rho = PyFloat_AsDouble(a[8]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+    if (a[9] != Py_None) USUAL(dh.set(a[9]) && dh.type == dy.type && fits(dh, dy.rows, dy.cols, dy.dev));
+    const int64_t ld = at_least_1(dy.cols);
+    at::Tensor da = empty({dy.rows, dy.cols}, dy, dy.type), dx = empty({dy.rows, dy.cols}, dy, dy.type);
+    at::Tensor dwp = empty({dy.cols}, dy, w.pre->scalar_type()), dw = empty({dy.cols}, dy, w.pre->scalar_type()), dg;
+    if (gate.t) dg = empty(gate.t->sizes(), dy, gate.t->scalar_type());
+    const size_t need = f_sandwich_workspace(dy.rows, dy.cols);
+    at::Tensor ws = empty({static_cast<int64_t>(need / 4)}, dy, at::kFloat);
+    USUAL(queue(f_sandwich_backward, dy.rows, dy.cols, static_cast<float>(rho), dy.p, dy.ld, dh.p, dh.ld, type_code(dy.type),
+                A.m.p, type_code(A.m.type), A.m.ld, A.scales(), A.s.ld, H.m.p, type_code(H.m.type), H.m.ld, H.scales(),
+                H.s.ld, w.post->data_ptr(), w.pre->data_ptr(), w.type, gate.p, gate.ld, gate.type, gate.group,
+                tp->data_ptr<float>(), t->data_ptr<float>(), da.data_ptr(), ld, dx.data_ptr(), ld, dwp.data_ptr(),
+                dw.data_ptr(), dg.defined() ? dg.data_ptr() : nullptr, ld, ws.data_ptr(), need,
+                stream_of(dy.dev)) == SGEMM_SUCCESS);
+    return Py_BuildValue("(NNNNN)", wrap(std::move(da)), wrap(std::move(dx)), wrap(std::move(dwp)), wrap(std::move(dw)),
+                         wrap_or_none(std::move(dg)));
+  });
+}
+
+// (gate, up, 8-bit type, the checkpoints' 8-bit type or -1) -> (q, scale, gate8, up8)
+PyObject *swiglu(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    Matrix g, u;
+    USUAL(n == 4 && g.set(a[0]) && u.set(a[1]) && float_type(g.type) >= 0 && u.type == g.type &&
+          fits(u, g.rows, g.cols, g.dev) && current(g.dev));
+    const int tq = static_cast<int>(PyLong_AsLong(a[2])), tk = static_cast<int>(PyLong_AsLong(a[3]));
+    int64_t ldq;
+    at::Tensor q = empty_fp8(g.rows, g.cols, g, fp8_scalar(tq), ldq), s = empty({g.rows, blocks(g.cols)}, g, at::kFloat);
+    Checkpoints k;
+    k.make(g, tk);
+    USUAL(queue(f_swiglu, g.rows, g.cols, g.p, g.ld, u.p, u.ld, type_code(g.type), q.data_ptr(),
+                static_cast<sgemm_type_t>(tq), ldq, s.data_ptr<float>(), at_least_1(blocks(g.cols)), k.qp(0), k.ld, k.sp(0),
+                k.lds, k.qp(1), k.ld, k.sp(1), k.lds, static_cast<sgemm_type_t>(tk), stream_of(g.dev)) == SGEMM_SUCCESS);
+    return Py_BuildValue("(NNNN)", wrap(std::move(q)), wrap(std::move(s)), k.pair(0), k.pair(1));
+  });
+}
+
+// (dy, gate, up, 8-bit type of the gradient, of y) -> (q_rows, scale_rows, q_cols, scale_cols, y_cols, y_scale)
+PyObject *swiglu_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    Matrix dy;
+    KeptMatrix G, U;
+    USUAL(n == 5 && dy.set(a[0]) && float_type(dy.type) >= 0 && G.set(a[1], dy) && U.set(a[2], dy) && !G.s.t == !U.s.t &&
+          current(dy.dev));
+    const int tz = static_cast<int>(PyLong_AsLong(a[3])), ty = static_cast<int>(PyLong_AsLong(a[4]));
+    const int64_t kb = blocks(dy.cols), rb = blocks(dy.rows), wide = 2 * kb * SGEMM_FP8_BLOCK, ld = at_least_1(wide);
+    int64_t ldy;
+    at::Tensor qr = empty({dy.rows, wide}, dy, fp8_scalar(tz)), qc = empty({dy.rows, wide}, dy, fp8_scalar(tz));
+    at::Tensor sr = empty({dy.rows, 2 * kb}, dy, at::kFloat), sc = empty({rb, wide}, dy, at::kFloat);
+    at::Tensor qy = empty_fp8(dy.rows, dy.cols, dy, fp8_scalar(ty), ldy), sy = empty({rb, dy.cols}, dy, at::kFloat);
+    USUAL(queue(f_swiglu_backward, dy.rows, dy.cols, dy.p, dy.ld, type_code(dy.type), G.m.p, type_code(G.m.type), G.m.ld,
+                G.scales(), G.s.ld, U.m.p, type_code(U.m.type), U.m.ld, U.scales(), U.s.ld, static_cast<sgemm_type_t>(tz),
+                qr.data_ptr(), ld, sr.data_ptr<float>(), at_least_1(2 * kb), qc.data_ptr(), ld, sc.data_ptr<float>(), ld,
+                static_cast<sgemm_type_t>(ty), qy.data_ptr(), ldy, sy.data_ptr<float>(), at_least_1(dy.cols),
+                stream_of(dy.dev)) == SGEMM_SUCCESS);
+    return Py_BuildValue("(NNNNNN)", wrap(std::move(qr)), wrap(std::move(sr)), wrap(std::move(qc)), wrap(std::move(sc)),
+                         wrap(std::move(qy)), wrap(std::move(sy)));
+  });
+}
+
+// (q, scale, 8-bit type) -> (q, scale)
+PyObject *requantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    Matrix x, sx;
+    USUAL(n == 3 && x.set(a[0]) && sx.set(a[1]) && fp8_type(x.type) >= 0 && sx.type == at::kFloat &&
+          fits(sx, x.rows, blocks(x.cols), x.dev) && current(x.dev));
+    const int tq = static_cast<int>(PyLong_AsLong(a[2]));
+    int64_t ldq;
+    at::Tensor q = empty_fp8(x.rows, x.cols, x, fp8_scalar(tq), ldq), s = empty({blocks(x.rows), x.cols}, x, at::kFloat);
+    USUAL(queue(f_requantize, x.rows, x.cols, x.p, type_code(x.type), x.ld, static_cast<const float *>(sx.p), sx.ld,
+                q.data_ptr(), static_cast<sgemm_type_t>(tq), ldq, s.data_ptr<float>(), at_least_1(x.cols),
+                stream_of(x.dev)) == SGEMM_SUCCESS);
+    return Py_BuildValue("(NN)", wrap(std::move(q)), wrap(std::move(s)));
+  });
+}
+
 // The addresses of the C ABI's functions, in the order of the pointers above.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  void *f[6];
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
+  void *f[12];
+  if (n != 12) {
+    PyErr_SetString(PyExc_TypeError, "bind takes twelve addresses");
     return nullptr;
   }
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < 12; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -266,6 +478,12 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   f_norm = reinterpret_cast<decltype(f_norm)>(f[3]);
   f_norm_backward = reinterpret_cast<decltype(f_norm_backward)>(f[4]);
   f_workspace = reinterpret_cast<decltype(f_workspace)>(f[5]);
+  f_sandwich = reinterpret_cast<decltype(f_sandwich)>(f[6]);
+  f_sandwich_backward = reinterpret_cast<decltype(f_sandwich_backward)>(f[7]);
+  f_sandwich_workspace = reinterpret_cast<decltype(f_sandwich_workspace)>(f[8]);
+  f_swiglu = reinterpret_cast<decltype(f_swiglu)>(f[9]);
+  f_swiglu_backward = reinterpret_cast<decltype(f_swiglu_backward)>(f[10]);
+  f_requantize = reinterpret_cast<decltype(f_requantize)>(f[11]);
   Py_RETURN_NONE;
 }
 
@@ -279,6 +497,11 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<quantize_both>("quantize_both"),
                          method<norm>("norm"),
                          method<norm_backward>("norm_backward"),
+                         method<sandwich_norm>("sandwich_norm"),
+                         method<sandwich_norm_backward>("sandwich_norm_backward"),
+                         method<swiglu>("swiglu"),
+                         method<swiglu_backward>("swiglu_backward"),
+                         method<requantize>("requantize"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp8_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

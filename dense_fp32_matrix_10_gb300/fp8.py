@@ -76,7 +76,9 @@ def _library():
         else:
             _fp8_torch.bind(*(ctypes.cast(f, _VP).value for f in (
                 lib.sgemm_fp8, lib.sgemm_fp8_quantize, lib.sgemm_fp8_quantize_both, lib.sgemm_rms_norm_fp8,
-                lib.sgemm_rms_norm_backward, lib.sgemm_rms_norm_backward_workspace)))
+                lib.sgemm_rms_norm_backward, lib.sgemm_rms_norm_backward_workspace, lib.sgemm_sandwich_norm_fp8,
+                lib.sgemm_sandwich_norm_backward, lib.sgemm_sandwich_norm_backward_workspace, lib.sgemm_swiglu_fp8,
+                lib.sgemm_swiglu_backward_fp8, lib.sgemm_fp8_requantize)))
             _usual = _fp8_torch
         _lib = lib
     return _lib

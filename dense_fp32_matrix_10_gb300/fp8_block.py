@@ -167,6 +167,11 @@ def sandwich_norm_fp8(a, x, post_weight, weight, gate=None, residual_scale=1.0, 
     it has a's number of rows).  post_weight, weight and gate are float32 or of a's type.  With training=True also
     post_rstd and rstd, which sandwich_norm_backward wants (not set for rows without elements); with `checkpoint` an
     8-bit type also the checkpoints of a and h in it."""
+    if fp8._usual is not None and stream is None and dtype in _FP8:
+        r = fp8._usual.sandwich_norm(a, x, post_weight, weight, gate, residual_scale, eps, _FP8[dtype], training,
+                                     -1 if checkpoint is None else _fp8_type(checkpoint))
+        if r is not None:
+            return SandwichNormFp8._make(r)
     px, rows, cols, lda, tx, dev = _mat(a, "a", _FLOAT)
     pr, _, _, ldx, _, devx = _like(x, "x", rows, cols, _SAME[tx])
     tq = _fp8_type(dtype)
@@ -207,6 +212,10 @@ def sandwich_norm_backward(dy, a, h, post_weight, weight, post_rstd, rstd, gate=
     `a` and `h` are the forward pass's matrices (of dy's type) or checkpoints of them, post_rstd and rstd what it
     returned; `dh` is the gradient that reaches h along the residual path.  da and dx are in dy's type, the others in
     those of what they are gradients of; dgate is summed over the rows that share a row of the gate."""
+    if fp8._usual is not None and stream is None:
+        r = fp8._usual.sandwich_norm_backward(dy, a, h, post_weight, weight, post_rstd, rstd, gate, residual_scale, dh)
+        if r is not None:
+            return SandwichNormGrad._make(r)
     pd, rows, cols, lddy, tx, dev = _mat(dy, "dy", _FLOAT)
     pa, ta, lda, psa, ldsa, deva = _kept(a, "a", rows, cols, _SAME[tx])
     ph, th, ldh, psh, ldsh, devh = _kept(h, "h", rows, cols, _SAME[tx])
@@ -245,6 +254,10 @@ def swiglu_fp8(gate, up, dtype=E4M3, checkpoint=None, stream=None):
 
     gate and up are of one type (the halves of one product's output, say).  With `checkpoint` an 8-bit type also the
     checkpoints of both in it, which swiglu_backward_fp8 takes."""
+    if fp8._usual is not None and stream is None and dtype in _FP8:
+        r = fp8._usual.swiglu(gate, up, _FP8[dtype], -1 if checkpoint is None else _fp8_type(checkpoint))
+        if r is not None:
+            return SwigluFp8._make(r)
     pg, rows, cols, ldg, tx, dev = _mat(gate, "gate", _FLOAT)
     pu, _, _, ldu, _, devu = _like(up, "up", rows, cols, _SAME[tx])
     _one_device(dev, devu)
@@ -278,6 +291,10 @@ def swiglu_backward_fp8(dy, gate, up, dtype=E4M3, y_dtype=E4M3, stream=None):
     the operand of a product with both projections' weights in one matrix, or by halves (q[:, :cols] and
     q[:, q.shape[1] // 2:][:, :cols], the scales likewise) of one with each.  y_cols is y in `y_dtype`, for the weight
     gradient of the projection that read it."""
+    if fp8._usual is not None and stream is None and dtype in _FP8 and y_dtype in _FP8:
+        r = fp8._usual.swiglu_backward(dy, gate, up, _FP8[dtype], _FP8[y_dtype])
+        if r is not None:
+            return SwigluGradFp8._make(r)
     pd, rows, cols, lddy, tx, dev = _mat(dy, "dy", _FLOAT)
     pg, tg, ldg, psg, ldsg, devg = _kept(gate, "gate", rows, cols, _SAME[tx])
     pu, tu, ldu, psu, ldsu, devu = _kept(up, "up", rows, cols, _SAME[tx])
@@ -304,6 +321,11 @@ def swiglu_backward_fp8(dy, gate, up, dtype=E4M3, y_dtype=E4M3, stream=None):
 def requantize_fp8(q, scale, dtype=None, stream=None):
     """(q, scale) in (128, 1) blocks of what a matrix in (1, 128) blocks stands for, in `dtype` (default: q's): a weight
     gradient's operand from the rows that the forward pass multiplied with."""
+    if fp8._usual is not None and stream is None:
+        to = _FP8.get(getattr(q, "dtype", None) if dtype is None else dtype, -1)
+        r = fp8._usual.requantize(q, scale, to) if to >= 0 else None
+        if r is not None:
+            return r
     pq, rows, cols, ldq, tx, dev = _mat(q, "q", _FP8)
     ps, _, _, lds, _, devs = _like(scale, "scale", rows, _cdiv(cols, BLOCK), _F32)
     _one_device(dev, devs)

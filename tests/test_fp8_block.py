@@ -689,6 +689,46 @@ def test_empty_matrices(sg, rows, cols):  # noqa: F811
     assert q.shape == (rows, cols) and s.shape == (cdiv(rows, B), cols)
 
 
+# ---------------------------------------------------------------- the extension module
+def test_extension_leaves_the_unusual_to_python(lib):
+    from dense_fp32_matrix_10_gb300 import fp8
+    e, x = fp8._usual, torch.zeros(4, 8)
+    w, t = x[0], x[:, 0]
+    assert e.sandwich_norm(x, x, w, w, None, 1.0, 1e-6, 8, True, 8) is None                   # not on a GPU
+    assert e.sandwich_norm_backward(x, (x, x), x, w, w, t, t, w, 1.0, None) is None
+    assert e.swiglu(x, x, 8, -1) is None and e.swiglu_backward(x, x, x, 8, 8) is None and e.requantize(x, x, 8) is None
+    assert e.sandwich_norm(None, None, w, w, 3, "1", 1e-6, 8, True, 8) is None                # not tensors
+    assert e.swiglu(x, x) is None and e.swiglu_backward(x, (x,), x, 8, 8) is None              # arguments missing
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(1, 128), (5, 0), (0, 7), (70, 333), (258, 1024)])
+def test_both_ways_through_python(sg, monkeypatch, shape):  # noqa: F811
+    """The extension module and the general code hand over the same calls."""
+    from dense_fp32_matrix_10_gb300 import fp8
+    rows, cols = shape
+    a, x, dy, dh = (randn(shape, 201 + i, torch.bfloat16) for i in range(4))
+    w, g, t = randn(cols, 205), randn((2, cols), 206, torch.bfloat16), randn(rows, 207).abs()
+    g = g if rows % 2 == 0 and rows else g[0]
+
+    def everything():
+        o = sg.sandwich_norm_fp8(a, x, w, w, gate=g, residual_scale=0.5, training=True, checkpoint=E5M2)
+        u = sg.swiglu_fp8(a, x, dtype=E5M2, checkpoint=E4M3)
+        out = [o.q, o.scale, o.h, *o.a8, *o.h8, u.q, u.scale, *u.gate8, *u.up8]
+        out += [o.post_rstd, o.rstd] if cols else []   # (rows of no elements have none)
+        out += sg.sandwich_norm_fp8(a, x, w, w)[:3]
+        out += sg.sandwich_norm_backward(dy, o.a8, o.h, w, w, t, t, gate=g, residual_scale=0.5, dh=dh)
+        out += sg.sandwich_norm_backward(dy, a, o.h8, w, w, t, t)[:4]
+        out += [*sg.swiglu_backward_fp8(dy, u.gate8, u.up8), *sg.swiglu_backward_fp8(dy, a, x, E5M2, E5M2)]
+        out += [*sg.requantize_fp8(u.q, u.scale), *sg.requantize_fp8(u.q, u.scale, E4M3)]
+        return out
+
+    ours = everything()
+    monkeypatch.setattr(fp8, "_usual", None)
+    for p, q in zip(ours, everything()):
+        assert p.stride() == q.stride() and same(p, q)
+
+
 # ---------------------------------------------------------------- refusals
 @pytest.fixture(scope="module")
 def lib(sg):  # noqa: F811
