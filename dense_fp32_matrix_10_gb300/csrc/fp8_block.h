@@ -71,7 +71,10 @@ struct SwigluGradParams {
   int64_t lddy, ldqr, ldsr, ldqc, ldsc, ldqy, ldsy, rows, cols;
   int typeX, z_e5m2, y_e5m2;
 };
-cudaError_t launch_swiglu_backward(const SwigluGradParams &p, cudaStream_t s);
+// (one for each type of dy)
+cudaError_t launch_swiglu_backward_f32(const SwigluGradParams &p, int sm_count, cudaStream_t s);
+cudaError_t launch_swiglu_backward_bf16(const SwigluGradParams &p, int sm_count, cudaStream_t s);
+cudaError_t launch_swiglu_backward_f16(const SwigluGradParams &p, int sm_count, cudaStream_t s);
 
 struct RequantizeParams {
   const unsigned char *x;

@@ -246,7 +246,7 @@ sgemm_status_t sgemm_swiglu_backward_fp8(
   if (!good_dim(rows) || !good_dim(cols) || !is_float_type(typeX) || !is_fp8_type(typeZ) || !is_fp8_type(typeY))
     return SGEMM_ERR_INVALID_VALUE;
   const int64_t kb = blocks_of(cols, SGEMM_FP8_BLOCK), wide = 2 * kb * SGEMM_FP8_BLOCK, rb = blocks_of(rows, SGEMM_FP8_BLOCK);
-  if (!good_dim(wide) || !SG != !SU || !good_kept(typeG, typeX, ldg, SG, ldsg, rows, cols) ||
+  if (!good_dim(wide) || !SG != !SU || typeG != typeU || !good_kept(typeG, typeX, ldg, SG, ldsg, rows, cols) ||
       !good_kept(typeU, typeX, ldu, SU, ldsu, rows, cols))
     return SGEMM_ERR_INVALID_VALUE;
   if (!good_ld(lddy, cols) || !good_ld(ldqr, wide) || !good_ld(ldsr, 2 * kb) || !good_ld(ldqc, wide) ||
@@ -267,7 +267,8 @@ sgemm_status_t sgemm_swiglu_backward_fp8(
   const sgemm_status_t st = check_ranges(r);
   if (st != SGEMM_SUCCESS) return st;
   sgemm_status_t why = SGEMM_SUCCESS;
-  if (!device_state(&why)) return why;
+  const DeviceState *d = device_state(&why);
+  if (!d) return why;
   SwigluGradParams p = {};
   p.dy = DY;
   p.g = kept(G, typeG, ldg, SG, ldsg);
@@ -290,7 +291,10 @@ sgemm_status_t sgemm_swiglu_backward_fp8(
   p.typeX = typeX;
   p.z_e5m2 = typeZ == SGEMM_TYPE_E5M2;
   p.y_e5m2 = typeY == SGEMM_TYPE_E5M2;
-  return queued(launch_swiglu_backward(p, reinterpret_cast<cudaStream_t>(stream)), 1);
+  const auto launch = typeX == SGEMM_TYPE_F32    ? launch_swiglu_backward_f32
+                      : typeX == SGEMM_TYPE_BF16 ? launch_swiglu_backward_bf16
+                                                 : launch_swiglu_backward_f16;
+  return queued(launch(p, d->sm_count, reinterpret_cast<cudaStream_t>(stream)), 1);
 }
 
 sgemm_status_t sgemm_fp8_requantize(int64_t rows, int64_t cols, const void *QX, sgemm_type_t typeX, int64_t ldqx,

@@ -427,7 +427,7 @@ PyObject *swiglu_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     Matrix dy;
     KeptMatrix G, U;
-    USUAL(n == 5 && dy.set(a[0]) && float_type(dy.type) >= 0 && G.set(a[1], dy) && U.set(a[2], dy) && !G.s.t == !U.s.t &&
+    USUAL(n == 5 && dy.set(a[0]) && float_type(dy.type) >= 0 && G.set(a[1], dy) && U.set(a[2], dy) && G.m.type == U.m.type &&
           current(dy.dev));
     const int tz = static_cast<int>(PyLong_AsLong(a[3])), ty = static_cast<int>(PyLong_AsLong(a[4]));
     const int64_t kb = blocks(dy.cols), rb = blocks(dy.rows), wide = 2 * kb * SGEMM_FP8_BLOCK, ld = at_least_1(wide);

@@ -286,7 +286,7 @@ def swiglu_backward_fp8(dy, gate, up, dtype=E4M3, y_dtype=E4M3, stream=None):
     """The gradient of silu(gate) * up as operands of the products that follow: SwigluGradFp8(q_rows, scale_rows, q_cols,
     scale_cols, y_cols, y_scale).
 
-    gate and up are the forward pass's matrices (of dy's type) or both checkpoints.  q_rows and q_cols hold
+    gate and up are the forward pass's matrices (of dy's type) or both checkpoints of one type.  q_rows and q_cols hold
     [dgate | dup] in `dtype`, each half as wide as cols rounded up to a multiple of 128 and zero behind its cols columns:
     the operand of a product with both projections' weights in one matrix, or by halves (q[:, :cols] and
     q[:, q.shape[1] // 2:][:, :cols], the scales likewise) of one with each.  y_cols is y in `y_dtype`, for the weight
@@ -298,8 +298,8 @@ def swiglu_backward_fp8(dy, gate, up, dtype=E4M3, y_dtype=E4M3, stream=None):
     pd, rows, cols, lddy, tx, dev = _mat(dy, "dy", _FLOAT)
     pg, tg, ldg, psg, ldsg, devg = _kept(gate, "gate", rows, cols, _SAME[tx])
     pu, tu, ldu, psu, ldsu, devu = _kept(up, "up", rows, cols, _SAME[tx])
-    if (psg is None) != (psu is None):
-        raise TypeError("gate and up must be both matrices or both checkpoints")
+    if tg != tu:
+        raise TypeError("gate and up must be both matrices or both checkpoints of one type")
     _one_device(dev, devg, devu)
     tz, ty = _fp8_type(dtype), _fp8_type(y_dtype)
     ctx = _on(stream, dev)

@@ -394,15 +394,15 @@ def halves(o, cols):
 @gpu
 @pytest.mark.parametrize("shape", UNIT_SHAPES)
 @pytest.mark.parametrize("dtype", FLOATS)
-@pytest.mark.parametrize("keep", [None, E4M3])
+@pytest.mark.parametrize("keep", [None, E4M3, E5M2])
 def test_unit_gradient(sg, shape, dtype, keep):  # noqa: F811
     rows, cols = shape
     g, u, dy = randn(shape, 111, dtype, 3.0), randn(shape, 112, dtype), randn(shape, 113, dtype, 0.01)
-    G, U_ = (g, u) if keep is None else (sg.quantize_fp8(g, dtype=keep), sg.quantize_fp8(u, dtype=E5M2))
+    G, U_ = (g, u) if keep is None else (sg.quantize_fp8(g, dtype=keep), sg.quantize_fp8(u, dtype=keep))
     vg, vu = (v.double() if keep is None else v[0].double() * spread(v[1], 1, B, rows, cols) for v in (G, U_))
     if keep is not None:   # q * scale is rounded to FP32
         vg, vu = vg.float().double(), vu.float().double()
-    o = sg.swiglu_backward_fp8(dy, G, U_, dtype=E5M2 if keep is None else E4M3, y_dtype=E4M3)
+    o = sg.swiglu_backward_fp8(dy, G, U_, dtype=E4M3 if keep == E4M3 else E5M2, y_dtype=E5M2 if keep == E5M2 else E4M3)
     y, Ey, fu, Eu, slope, Es = unit_bounds(vg, vu)
     d = dy.double()
     want = ((d * vu * slope, (d * vu).abs() * (Es + 3 * U * slope.abs())), (d * fu, d.abs() * (Eu + U * fu.abs())))
@@ -807,7 +807,7 @@ def unit_gradient_status(lib, rows=8, cols=256, DY=AT[0], lddy=256, tx=1, G=AT[1
 
 @pytest.mark.parametrize("change,status", [
     (dict(rows=-1), 1), (dict(cols=(1 << 30) + 1), 1), (dict(tx=8), 1), (dict(tz=1), 1), (dict(ty=0), 1), (dict(tg=8), 1),
-    (dict(SG=AT[9], tg=8), 1), (dict(SG=AT[9], SU=AT[10]), 1), (dict(SG=AT[9], SU=AT[10], tg=8, tu=9, ldsu=1), 1),
+    (dict(SG=AT[9], tg=8), 1), (dict(SG=AT[9], SU=AT[10]), 1), (dict(SG=AT[9], SU=AT[10], tg=8, tu=8, ldsu=1), 1), (dict(SG=AT[9], SU=AT[10], tg=8, tu=9), 1),
     (dict(DY=None), 1), (dict(G=None), 1), (dict(U_=None), 1), (dict(QR=None), 1), (dict(SR=None), 1), (dict(QC=None), 1),
     (dict(SC=None), 1), (dict(QY=None), 1), (dict(SY=None), 1), (dict(ldqr=511), 1), (dict(ldsr=3), 1), (dict(ldqc=511), 1),
     (dict(ldsc=511), 1), (dict(ldqy=255), 1), (dict(ldsy=255), 1), (dict(QR=AT[0]), 2), (dict(QC=AT[3] + 4000), 2),
@@ -845,7 +845,7 @@ def test_valid_calls_without_gpu_are_unsupported(lib):
     assert norms_status(lib, GATE=AT[4], group=1 << 40, QA=AT[8], SA=AT[9], TP=AT[10], T=AT[11]) == 3
     assert norms_gradient_status(lib, GATE=AT[12], group=3, DG=AT[13], SA=AT[14], ta=8, DH=AT[15]) == 3
     assert norms_gradient_status(lib, DWP=None, DW=None, ws=None) == 3
-    assert unit_gradient_status(lib, SG=AT[9], SU=AT[10], tg=8, tu=9) == 3
+    assert unit_gradient_status(lib, SG=AT[9], SU=AT[10], tg=9, tu=9) == 3
 
 
 def test_tensors_are_checked_before_any_call(sg):  # noqa: F811
@@ -890,7 +890,7 @@ def test_tensors_that_do_not_fit_are_refused(sg):  # noqa: F811
     for args, error, match in [((x, y), ValueError, "up must be"), ((x, h), TypeError, "up must be")]:
         with pytest.raises(error, match=match):
             sg.swiglu_fp8(*args)
-    for args, error, match in [((x, y, x), ValueError, "gate must be"), ((x, k, x), TypeError, "both"), ((h, x, x), TypeError, "gate must be")]:
+    for args, error, match in [((x, y, x), ValueError, "gate must be"), ((x, k, x), TypeError, "both"), ((x, k, sg.quantize_fp8(x, dtype=E5M2)), TypeError, "one type"), ((h, x, x), TypeError, "gate must be")]:
         with pytest.raises(error, match=match):
             sg.swiglu_backward_fp8(*args)
     with pytest.raises(ValueError, match="scale must be"):
