@@ -190,25 +190,30 @@ __device__ __forceinline__ void copies_wait(int n) {
   else
     asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
-// Sixteen elements of T in 16-byte units `step` apart.
+// A thread's 16-byte units lie a warp's width apart: no bank conflicts, and constant offsets from its first.
+constexpr int kUnitStep = 32;
+__device__ __forceinline__ int first_unit(int units) {   // of this thread, where each has `units` of them
+  return (threadIdx.x >> 5) * units * kUnitStep + (threadIdx.x & 31);
+}
+// Sixteen elements of T in sizeof(T) units.
 template <class T>
-__device__ __forceinline__ void copy16(uint4 *to, int step, const T *x, int n, int level) {
+__device__ __forceinline__ void copy16(uint4 *to, const T *x, int n, int level) {
   constexpr int U = sizeof(T);
   if (n >= 16 && level) {
 #pragma unroll
-    for (int k = 0; k < U; ++k) copy_16(to + k * step, reinterpret_cast<const uint4 *>(x) + k);
+    for (int k = 0; k < U; ++k) copy_16(to + k * kUnitStep, reinterpret_cast<const uint4 *>(x) + k);
   } else {
     const Raw16<T> r = load16(x, n, level);
 #pragma unroll
-    for (int k = 0; k < U; ++k) to[k * step] = r.half[k / (U / 2)].u[k % (U / 2)];
+    for (int k = 0; k < U; ++k) to[k * kUnitStep] = r.half[k / (U / 2)].u[k % (U / 2)];
   }
 }
 template <class T>
-__device__ __forceinline__ Raw16<T> take16(const uint4 *at, int step) {
+__device__ __forceinline__ Raw16<T> take16(const uint4 *at) {
   constexpr int U = sizeof(T);
   Raw16<T> r;
 #pragma unroll
-  for (int k = 0; k < U; ++k) r.half[k / (U / 2)].u[k % (U / 2)] = at[k * step];
+  for (int k = 0; k < U; ++k) r.half[k / (U / 2)].u[k % (U / 2)] = at[k * kUnitStep];
   return r;
 }
 // Sixteen elements of a checkpoint, one unit, and their scale.

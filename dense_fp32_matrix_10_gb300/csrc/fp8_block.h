@@ -36,7 +36,7 @@ struct SandwichParams {
   int typeX, w_f32, e5m2, keep_e5m2;
   float eps, residual_scale;
 };
-cudaError_t launch_sandwich_norm(const SandwichParams &p, int sm_count, cudaStream_t s);
+cudaError_t launch_sandwich_norm(const SandwichParams &p, cudaStream_t s);
 
 struct SandwichGradParams {
   const void *dy, *dh, *wp, *w;
@@ -48,6 +48,8 @@ struct SandwichGradParams {
   int64_t lddy, lddh, ldda, lddx, lddgate, rows, cols;
   int typeX, w_f32;
   float residual_scale;
+  uint64_t wait_budget_ns;
+  int *status;
 };
 // Floats of workspace.
 int64_t sandwich_partials(int64_t rows, int64_t cols);

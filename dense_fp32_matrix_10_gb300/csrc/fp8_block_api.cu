@@ -75,8 +75,7 @@ sgemm_status_t sgemm_sandwich_norm_fp8(
   const sgemm_status_t st = check_ranges(r);
   if (st != SGEMM_SUCCESS) return st;
   sgemm_status_t why = SGEMM_SUCCESS;
-  DeviceState *d = device_state(&why);
-  if (!d) return why;
+  if (!device_state(&why)) return why;
   SandwichParams p = {};
   p.a = A;
   p.x = X;
@@ -109,7 +108,7 @@ sgemm_status_t sgemm_sandwich_norm_fp8(
   p.keep_e5m2 = typeKeep == SGEMM_TYPE_E5M2;
   p.eps = eps;
   p.residual_scale = residual_scale;
-  return queued(launch_sandwich_norm(p, d->sm_count, reinterpret_cast<cudaStream_t>(stream)), 1);
+  return queued(launch_sandwich_norm(p, reinterpret_cast<cudaStream_t>(stream)), 1);
 }
 
 size_t sgemm_sandwich_norm_backward_workspace(int64_t rows, int64_t cols) {
@@ -161,7 +160,8 @@ sgemm_status_t sgemm_sandwich_norm_backward(
   const sgemm_status_t st = check_ranges(r);
   if (st != SGEMM_SUCCESS) return st;
   sgemm_status_t why = SGEMM_SUCCESS;
-  if (!device_state(&why)) return why;
+  DeviceState *d = device_state(&why);
+  if (!d) return why;
   SandwichGradParams p = {};
   p.dy = DY;
   p.dh = DH;
@@ -176,7 +176,7 @@ sgemm_status_t sgemm_sandwich_norm_backward(
   p.dx = DX;
   p.dwp = DWP;
   p.dw = DW;
-  p.dgate = DGATE;
+  p.dgate = rows > 0 ? DGATE : nullptr;
   p.partial = sums ? static_cast<float *>(workspace) : nullptr;
   p.lddy = lddy;
   p.lddh = lddh;
@@ -188,6 +188,8 @@ sgemm_status_t sgemm_sandwich_norm_backward(
   p.typeX = typeX;
   p.w_f32 = typeW == SGEMM_TYPE_F32;
   p.residual_scale = residual_scale;
+  p.wait_budget_ns = g_wait_budget_ns.load(std::memory_order_relaxed);
+  p.status = d->status;
   int launches = 0;
   const cudaError_t err = launch_sandwich_norm_backward(p, reinterpret_cast<cudaStream_t>(stream), &launches);
   return queued(err, launches);

@@ -1,42 +1,147 @@
 // sandwich_backward.cu -- the gradient of the norms around a block
 // (sandwich_norm.cuh has the formulas).
 //
+// A row is 16 consecutive elements a thread, 128 threads a CTA and, where it
+// has more than 2048 elements, up to eight CTAs of a cluster.  A cluster takes
+// consecutive rows one after the other: the row's weights and the sums over
+// rows stay in registers (64 of a thread's 128), and a thread copies its own
+// elements of the next rows to places of its own in shared memory.  An SM's
+// CTAs belong to different rows, which are in different phases.
+//
 // The second mean is that of a sum which is linear in the first, so both come
 // from three sums over the row, taken together:
 //   A = sum dy w h,  P = sum (t dy w + dh) p,  R = sum h p   with p = gate wp a
 //   sum v a = P - t^3 (A / cols) R
+#include <mutex>
+
 #include "sandwich_norm.cuh"
 
 namespace sg {
 namespace {
 
 constexpr int kSms = 152;   // of a GB300: sizes the partial sums, whose number must not depend on the device
+constexpr int kClusterThreads = 128, kMaxCluster = 8;   // of a CTA; CTAs of a row
+constexpr int kRowSmem = 224 * 1024;                    // of an SM for the copied rows
+constexpr int kLongThreads = 512, kLongElements = 16 * kLongThreads;   // of a segment of a longer row
 
-// The workspace: for every CTA a row of `pitch` floats for each of dw, dwp, and dgate's sums over the rows of the first
-// and of the last gate row that it shares with other CTAs.
+// Clusters, each with `rows` consecutive rows (the last one fewer), and their CTAs.
+struct Split {
+  unsigned clusters, rows, cluster;
+};
+
+// The workspace: for every cluster a row of `pitch` floats for each of dw, dwp, and dgate's sums over the rows of the first
+// and of the last gate row that it shares with other clusters.
 enum : int { kDw = 0, kDwp = 1, kHead = 2, kTail = 3, kParts = 4 };
 inline __host__ __device__ int64_t part_pitch(int64_t cols) { return (cols + 15) / 16 * 16; }
-__device__ __forceinline__ float *part(const SandwichGradParams &p, unsigned cta, int kind, int64_t c) {
-  return p.partial + (static_cast<int64_t>(cta) * kParts + kind) * part_pitch(p.cols) + c;
+__device__ __forceinline__ float *part(const SandwichGradParams &p, unsigned stream, int kind, int64_t c) {
+  return p.partial + (static_cast<int64_t>(stream) * kParts + kind) * part_pitch(p.cols) + c;
 }
 __device__ __forceinline__ void load_part(const float *at, float2 (&v)[8]) { unpack(load16(at, 16, 1), v); }
 __device__ __forceinline__ void store_part(float *at, const float2 (&v)[8]) { store16(at, v, 16, 1); }
 
-// What a row's sums over rows add up to at the end of a CTA's rows of a gate row (`group`, whose gate wp m goes with): its
-// part of dwp is added to the CTA's, and its part of dgate is stored, or dgate itself if all its rows are this CTA's.
-template <class T>
-__device__ __forceinline__ void flush(const SandwichGradParams &p, unsigned group, unsigned r0, unsigned r1, int64_t c, int n,
-                                      const float2 (&sn)[8], bool first, uint32_t vec) {
-  float2 v[8];
-  if (p.gate.p) {
-    load16_w<T>(p.gate.p, p.gate.f32, group * p.gate.ld + c, n, level(vec, 4), v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], sn[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = sn[i];
+// The three sums of a row over its threads, in a fixed order: in a warp as in RowSums, then every warp leaves its sums with
+// every CTA of the cluster, by stores that count towards an mbarrier there (a cluster barrier would wait for the stores to
+// memory, too: 8192 x 8192 284 instead of 254 us).  Used by turns, so that nothing is overwritten that a slower warp still
+// reads: a warp's sums of call i + 1 show that it has read those of call i.
+struct ClusterTotals {
+  float red[2][4][32];   // [turn][value][warp]; zero where there is none
+  uint64_t bar[2];
+};
+class ClusterSums {
+  ClusterTotals *sh;
+  unsigned cluster, calls = 0;
+  bool ok = true;
+  uint64_t budget_ns;
+  int *status;
+
+ public:
+  unsigned rank;
+
+  __device__ __forceinline__ ClusterSums(ClusterTotals *shared, unsigned cluster_size, uint64_t budget, int *device_status)
+      : sh(shared), cluster(cluster_size), budget_ns(budget), status(device_status),
+        rank(cluster_size > 1 ? cluster_ctarank() : 0) {
+    for (int i = threadIdx.x; i < 2 * 4 * 32; i += blockDim.x) (&sh->red[0][0][0])[i] = 0.0f;
+    if (cluster > 1) {
+      if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&sh->bar[0]), 1);
+        mbar_init(smem_u32(&sh->bar[1]), 1);
+        fence_mbar_init();
+      }
+      cluster_sync();   // (every CTA of the cluster is there to be written to)
+    } else {
+      __syncthreads();
+    }
   }
-  float *dwp = part(p, blockIdx.x, kDwp, c);
+  // False (for the whole warp) if the other warps' sums did not come in time.  The warp then sends and expects nothing more
+  // and the caller leaves its loop, so that the others run out of time as well and come to finish().
+  __device__ __forceinline__ bool operator()(float (&v)[4]) {
+    const int lane = threadIdx.x & 31, own = lane / 8, j = lane % 8;
+#pragma unroll
+    for (int k = 2, d = 16; k > 0; k >>= 1, d >>= 1) {
+      const bool upper = lane & d;
+#pragma unroll
+      for (int i = 0; i < k; ++i) {
+        const float mine = upper ? v[k + i] : v[i], give = upper ? v[i] : v[k + i];
+        v[i] = mine + __shfl_xor_sync(~0u, give, d);
+      }
+    }
+    float s = v[0];
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+    const unsigned warps = blockDim.x >> 5, turn = calls & 1;
+    if (cluster > 1 || warps > 1) {
+      float *to = &sh->red[turn][own][rank * warps + (threadIdx.x >> 5)];
+      if (cluster > 1) {
+        const uint32_t bar = smem_u32(&sh->bar[turn]);
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cluster * warps * 16);
+        if (j < static_cast<int>(cluster))
+          asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
+                           map_to_rank(smem_u32(to), j)),
+                       "r"(__float_as_uint(s)), "r"(map_to_rank(bar, j))
+                       : "memory");
+        ok = __all_sync(~0u, wait_parity_bounded(bar, calls >> 1 & 1, budget_ns, status));
+        if (!ok) return false;
+      } else {
+        if (j == 0) *to = s;
+        __syncthreads();
+      }
+      const float4 u = *reinterpret_cast<const float4 *>(&sh->red[turn][own][4 * j]);
+      s = (u.x + u.y) + (u.z + u.w);
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+      ++calls;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(~0u, s, 8 * i);
+    return true;
+  }
+  // Before the CTA ends: no warp of the cluster sends anything more, and what was sent has arrived (it was waited for; after
+  // a wait that ran out, some time is given to it).
+  __device__ __forceinline__ void finish() {
+    if (cluster == 1) return;
+    cluster_sync();
+    if (!ok)
+      for (int i = 0; i < 100; ++i) __nanosleep(1000);
+  }
+};
+
+// Whether all rows have one gate (or none): then dwp and dgate follow from one sum, which lies in dwp's place.
+__host__ __device__ inline bool one_gate(const SandwichGradParams &p) { return !p.gate.p || p.gate.rows >= p.rows; }
+
+// What a row's sums over rows add up to at the end of a cluster's (`stream`'s) rows r0 .. r1 - 1 of a gate row (`group`): its
+// part of dwp is added to the cluster's, and its part of dgate is stored, or dgate itself if all its rows are here.
+template <class T>
+__device__ __forceinline__ void flush(const SandwichGradParams &p, unsigned stream, unsigned group, unsigned r0, unsigned r1, int64_t c, int n,
+                                      const float2 (&sn)[8], bool first, uint32_t vec) {
+  if (one_gate(p)) {
+    store_part(part(p, stream, kDwp, c), sn);
+    return;
+  }
+  float2 v[8];
+  load16_w<T>(p.gate.p, p.gate.f32, group * p.gate.ld + c, n, level(vec, 4), v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], sn[i]);
+  float *dwp = part(p, stream, kDwp, c);
   if (!first) {
     float2 old[8];
     load_part(dwp, old);
@@ -56,7 +161,7 @@ __device__ __forceinline__ void flush(const SandwichGradParams &p, unsigned grou
     else
       store16(static_cast<T *>(p.dgate) + at, v, n, level(vec, 9));
   } else {
-    store_part(part(p, blockIdx.x, g0 < r0 ? kHead : kTail, c), sn);
+    store_part(part(p, stream, g0 < r0 ? kHead : kTail, c), sn);
   }
 }
 
@@ -71,8 +176,10 @@ __device__ __forceinline__ void load_gated(const SandwichGradParams &p, unsigned
     for (int i = 0; i < 8; ++i) m[i] = mul2(m[i], g[i]);
   }
 }
+// KIND: 1 E4M3, 2 E5M2, 3 one of them
+template <int KIND>
 __device__ __forceinline__ void unpack_kept(uint4 u, float scale, bool e5m2, float2 (&v)[8]) {
-  if (e5m2)
+  if (KIND == 3 ? e5m2 : KIND == 2)
     unpack_fp8<true>(u, v);
   else
     unpack_fp8<false>(u, v);
@@ -124,62 +231,77 @@ __device__ __forceinline__ void finish(const SandwichGradParams &p, int64_t row,
   store16(static_cast<T *>(p.dx) + row * p.lddx + c, dx, n, level(vec, 6));
 }
 
-// KA, KH: a and h are checkpoints.  vec: 0 dy, 1 dh, 2 w, 3 wp, 4 gate, 5 da, 6 dx, 7 a, 8 h, 9 dgate
-template <class T, bool KA, bool KH>
+// KIND: a and h are 0 matrices of T, 1 checkpoints in E4M3, 2 in E5M2, 3 any of these, each its own.
+// vec: 0 dy, 1 dh, 2 w, 3 wp, 4 gate, 5 da, 6 dx, 7 a, 8 h, 9 dgate
+template <class T, int KIND>
 struct RowPlaces {
-  static constexpr int U = sizeof(T), kDh = U, kA = 2 * U, kH = kA + (KA ? 1 : U), kUnits = kH + (KH ? 1 : U);
-  static constexpr int kScales = (KA ? 1 : 0) + (KH ? 1 : 0), kBytes = kUnits * 16 + kScales * 4;   // of a thread
+  static constexpr int U = sizeof(T), K = KIND == 1 || KIND == 2 ? 1 : U;   // 16-byte units of sixteen elements
+  static constexpr int kDh = U, kA = 2 * U, kH = kA + K, kUnits = kH + K;
+  static constexpr int kBytes = kUnits * 16 + (KIND ? 8 : 0);               // of a thread, with its scales
 };
-template <class T, bool KA, bool KH>
-__global__ void __launch_bounds__(kRowThreads, 1) sandwich_backward_kernel(const SandwichGradParams p, const Split split,
+template <class T, int KIND>
+__global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(const SandwichGradParams p, const Split split,
                                                                            const int depth, const uint32_t vec) {
-  using At = RowPlaces<T, KA, KH>;
-  extern __shared__ __align__(16) uint4 rows_smem[];   // [depth][dy, dh, a, h][thread], then [depth][scales of checkpoints][thread]
-  __shared__ float red[2][4][16];
+  using At = RowPlaces<T, KIND>;
+  extern __shared__ __align__(16) uint4 rows_smem[];   // [depth][warp][dy, dh, a, h][lane], then [depth][a's, h's scale][thread]
+  __shared__ __align__(16) ClusterTotals shared;
+  ClusterSums row_sums(&shared, split.cluster, p.wait_budget_ns, p.status);
   griddep_wait();
   griddep_launch_dependents();
-  const int step = blockDim.x;
-  const unsigned r0 = blockIdx.x * split.rows;
+  const unsigned stream = blockIdx.x / split.cluster;
+  const unsigned r0 = stream * split.rows;
   const unsigned r1 = static_cast<unsigned>(min(static_cast<int64_t>(r0) + split.rows, p.rows));
-  const int64_t c = threadIdx.x * 16;
-  const int n = static_cast<int>(max(int64_t(0), min(int64_t(16), p.cols - c)));
-  uint4 *mine = rows_smem + threadIdx.x;
-  float *scales = reinterpret_cast<float *>(rows_smem + depth * At::kUnits * step) + threadIdx.x;
+  const unsigned c = (row_sums.rank * blockDim.x + threadIdx.x) * 16;
+  const int n = max(0, min(16, static_cast<int>(p.cols) - static_cast<int>(c)));
+  uint4 *mine = rows_smem + first_unit(At::kUnits);
+  const unsigned step = blockDim.x * At::kUnits;
+  float *scales = reinterpret_cast<float *>(rows_smem + depth * step) + threadIdx.x;
+  // Whether this thread's elements of every input are copied asynchronously in whole units.
+  const bool fast = n == 16 && level(vec, 0) && (!p.dh || level(vec, 1)) &&
+                    (KIND == 0 ? level(vec, 7) && level(vec, 8) : KIND < 3 && level(vec, 7) == 2 && level(vec, 8) == 2);
   const auto fetch = [&](unsigned row, int slot) {
     if (row < r1) {
-      uint4 *to = mine + slot * At::kUnits * step;
-      float *s = scales + slot * At::kScales * step;
-      copy16(to, step, static_cast<const T *>(p.dy) + row * p.lddy + c, n, level(vec, 0));
-      if (p.dh) copy16(to + At::kDh * step, step, static_cast<const T *>(p.dh) + row * p.lddh + c, n, level(vec, 1));
-      const auto matrix = [&](const Kept &k, bool kept, int lv, uint4 *place, float *scale) {
-        if (kept)
+      uint4 *to = mine + slot * step;
+      float *s = scales + slot * 2 * blockDim.x;
+      const T *dy = static_cast<const T *>(p.dy) + row * p.lddy + c, *dh = static_cast<const T *>(p.dh) + row * p.lddh + c;
+      const auto matrix = [&](const Kept &k, int n, int lv, uint4 *place, float *scale) {
+        if (KIND == 3 ? k.s != nullptr : KIND != 0)
           copy16_kept(place, scale, static_cast<const unsigned char *>(k.p) + row * k.ld + c, k.s + row * k.lds + (c >> 7), n, lv);
         else
-          copy16(place, step, static_cast<const T *>(k.p) + row * k.ld + c, n, lv);
+          copy16(place, static_cast<const T *>(k.p) + row * k.ld + c, n, lv);
       };
-      matrix(p.a, KA, level(vec, 7), to + At::kA * step, s);
-      matrix(p.h, KH, level(vec, 8), to + At::kH * step, s + (KA ? step : 0));
+      if (fast) {
+        copy16(to, dy, 16, 1);
+        if (p.dh) copy16(to + At::kDh * kUnitStep, dh, 16, 1);
+        matrix(p.a, 16, 2, to + At::kA * kUnitStep, s);
+        matrix(p.h, 16, 2, to + At::kH * kUnitStep, s + blockDim.x);
+      } else {
+        copy16(to, dy, n, level(vec, 0));
+        if (p.dh) copy16(to + At::kDh * kUnitStep, dh, n, level(vec, 1));
+        matrix(p.a, n, level(vec, 7), to + At::kA * kUnitStep, s);
+        matrix(p.h, n, level(vec, 8), to + At::kH * kUnitStep, s + blockDim.x);
+      }
     }
     copies_commit();
   };
   const auto take = [&](int slot, Inputs &x) {
-    const uint4 *at = mine + slot * At::kUnits * step;
-    const float *s = scales + slot * At::kScales * step;
-    unpack(take16<T>(at, step), x.dy);
+    const uint4 *at = mine + slot * step;
+    const float *s = scales + slot * 2 * blockDim.x;
+    unpack(take16<T>(at), x.dy);
     if (p.dh) {
-      unpack(take16<T>(at + At::kDh * step, step), x.dh);
+      unpack(take16<T>(at + At::kDh * kUnitStep), x.dh);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x.dh[i] = both(0.0f);
     }
-    if constexpr (KA)
-      unpack_kept(at[At::kA * step], s[0], p.a.e5m2, x.a);
-    else
-      unpack(take16<T>(at + At::kA * step, step), x.a);
-    if constexpr (KH)
-      unpack_kept(at[At::kH * step], s[KA ? step : 0], p.h.e5m2, x.h);
-    else
-      unpack(take16<T>(at + At::kH * step, step), x.h);
+    const auto matrix = [&](const Kept &k, const uint4 *place, const float *scale, float2 (&v)[8]) {
+      if (KIND == 3 ? k.s != nullptr : KIND != 0)
+        unpack_kept<KIND>(*place, *scale, k.e5m2, v);
+      else
+        unpack(take16<T>(place), v);
+    };
+    matrix(p.a, at + At::kA * kUnitStep, s, x.a);
+    matrix(p.h, at + At::kH * kUnitStep, s + blockDim.x, x.h);
   };
   for (int d = 0; d < depth; ++d) fetch(r0 + d, d);
   float2 w[8], m[8], sw[8], sn[8];
@@ -189,7 +311,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) sandwich_backward_kernel(const
   unsigned group = p.gate.p ? r0 / p.gate.rows : 0, group_end = p.gate.p ? (group + 1) * p.gate.rows : ~0u;
   load_gated<T>(p, group, c, n, vec, m);
   const float mean = 1.0f / static_cast<float>(p.cols);
-  int turn = 0, slot = 0;
+  int slot = 0;
   bool first = true;
   float t_next = p.t[r0], tp_next = p.tp[r0];
   for (unsigned row = r0; row < r1; ++row) {
@@ -204,44 +326,45 @@ __global__ void __launch_bounds__(kRowThreads, 1) sandwich_backward_kernel(const
       t_next = p.t[row + 1];
       tp_next = p.tp[row + 1];
     }
-    float A = 0.0f, P = 0.0f, R = 0.0f;
+    float total[4] = {};
     {
       Inputs x;
       take(slot, x);
-      add_sums(x, w, m, t, A, P, R);
+      add_sums(x, w, m, t, total[0], total[1], total[2]);
     }
-    row_totals(A, P, R, red, turn);
-    asm volatile("" ::: "memory");   // (read again: the row's 64 values do not stay in registers meanwhile)
+    if (!row_sums(total)) break;
+    asm volatile("" ::: "memory");   // (read again: the row's values do not stay in registers meanwhile)
     {
       Inputs x;
       take(slot, x);
-      finish<T>(p, row, c, n, x, w, m, factors(t, tp, A, P, R, mean), sw, sn, vec);
+      finish<T>(p, row, c, n, x, w, m, factors(t, tp, total[0], total[1], total[2], mean), sw, sn, vec);
     }
     fetch(row + depth, slot);
     slot = slot + 1 == depth ? 0 : slot + 1;
     if (p.partial && (row + 1 == r1 || row + 1 == group_end)) {
-      if (n > 0) flush<T>(p, group, r0, r1, c, n, sn, first, vec);
+      if (n > 0) flush<T>(p, stream, group, r0, r1, c, n, sn, first, vec);
       first = false;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sn[i] = both(0.0f);
     }
   }
   copies_wait(0);
-  if (p.partial && n > 0) store_part(part(p, blockIdx.x, kDw, c), sw);
+  if (p.partial && n > 0) store_part(part(p, stream, kDw, c), sw);
+  row_sums.finish();
 }
 
-// Rows of more than 8192 elements, in segments of that many, read twice.  The sums over rows are kept in this CTA's rows
+// Rows of more than 16384 elements, in segments of 8192, read twice.  The sums over rows are kept in this CTA's rows
 // of the workspace, that of H a tp in kTail until its gate row ends.
 template <class T>
-__global__ void __launch_bounds__(kRowThreads, 1) sandwich_backward_long_kernel(const SandwichGradParams p, const Split split,
+__global__ void __launch_bounds__(kLongThreads, 1) sandwich_backward_long_kernel(const SandwichGradParams p, const Split split,
                                                                                 const uint32_t vec) {
-  __shared__ float red[2][4][16];
+  __shared__ __align__(16) float red[2][4][32];
   griddep_wait();
   griddep_launch_dependents();
+  RowSums<4> row_sums(red);
   const unsigned r0 = blockIdx.x * split.rows;
   const unsigned r1 = static_cast<unsigned>(min(static_cast<int64_t>(r0) + split.rows, p.rows));
   const float mean = 1.0f / static_cast<float>(p.cols);
-  int turn = 0;
   bool first = true;
   Inputs x;
   float2 w[8], m[8];
@@ -256,7 +379,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) sandwich_backward_long_kernel(
     }
     const auto matrix = [&](const Kept &k, int lv, float2 (&v)[8]) {
       if (k.s)
-        unpack_kept(load16_fp8(static_cast<const unsigned char *>(k.p) + row * k.ld + c, n, lv), k.s[row * k.lds + (c >> 7)],
+        unpack_kept<3>(load16_fp8(static_cast<const unsigned char *>(k.p) + row * k.ld + c, n, lv), k.s[row * k.lds + (c >> 7)],
                     k.e5m2, v);
       else
         unpack(load16(static_cast<const T *>(k.p) + row * k.ld + c, n, lv), v);
@@ -270,16 +393,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) sandwich_backward_long_kernel(
   for (unsigned row = r0; row < r1; ++row) {
     const float t = p.t[row], tp = p.tp[row];
     const unsigned group = p.gate.p ? row / p.gate.rows : 0;
-    float A = 0.0f, P = 0.0f, R = 0.0f;
-    for (int64_t c = threadIdx.x * 16; c < p.cols; c += kRowElements) {
+    float total[4] = {};
+    for (int64_t c = threadIdx.x * 16; c < p.cols; c += kLongElements) {
       load(row, group, c);
-      add_sums(x, w, m, t, A, P, R);
+      add_sums(x, w, m, t, total[0], total[1], total[2]);
     }
-    row_totals(A, P, R, red, turn);
-    const Factors f = factors(t, tp, A, P, R, mean);
+    row_sums(total);
+    const Factors f = factors(t, tp, total[0], total[1], total[2], mean);
     const bool begins = row == r0 || (p.gate.p && row % p.gate.rows == 0);
     const bool ends = row + 1 == r1 || (p.gate.p && (row + 1) % p.gate.rows == 0);
-    for (int64_t c = threadIdx.x * 16; c < p.cols; c += kRowElements) {
+    for (int64_t c = threadIdx.x * 16; c < p.cols; c += kLongElements) {
       const int n = load(row, group, c);
       float2 sw[8], sn[8];
 #pragma unroll
@@ -290,7 +413,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) sandwich_backward_long_kernel(
       if (!p.partial) continue;
       store_part(part(p, blockIdx.x, kDw, c), sw);
       if (ends)
-        flush<T>(p, group, r0, r1, c, n, sn, first, vec);
+        flush<T>(p, blockIdx.x, group, r0, r1, c, n, sn, first, vec);
       else
         store_part(part(p, blockIdx.x, kTail, c), sn);
     }
@@ -298,15 +421,15 @@ __global__ void __launch_bounds__(kRowThreads, 1) sandwich_backward_long_kernel(
   }
 }
 
-// Sums over CTAs in a fixed order: blockIdx.y 0 of dw, 1 of dwp, then of the gate rows that several CTAs share, which
-// are found by the gate row (by_group) or by the boundary between two CTAs.
+// Sums over clusters in a fixed order: blockIdx.y 0 of dw, 1 of dwp (and dgate, if it has one row), then of the gate rows
+// that several clusters share, which are found by the gate row (by_group) or by the boundary between two clusters.
 template <class T>
 __global__ void __launch_bounds__(1024) sandwich_sums_kernel(const SandwichGradParams p, const Split split,
                                                              const bool by_group) {
   __shared__ float red[32][33];
   griddep_wait();
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-  unsigned first = 0, end = split.ctas, group = 0;
+  unsigned first = 0, end = split.clusters, group = 0;
   if (blockIdx.y >= 2) {
     group = blockIdx.y - 2;
     if (!by_group) {
@@ -320,7 +443,7 @@ __global__ void __launch_bounds__(1024) sandwich_sums_kernel(const SandwichGradP
     first = static_cast<unsigned>(g0 / split.rows);
     end = static_cast<unsigned>((g1 - 1) / split.rows) + 1;
     if (first + 1 == end) return;
-  } else if (!(blockIdx.y ? p.dwp : p.dw)) {
+  } else if (blockIdx.y ? !p.dwp && !(p.dgate && one_gate(p)) : !p.dw) {
     return;
   }
   const auto kind = [&](unsigned b) {
@@ -344,29 +467,73 @@ __global__ void __launch_bounds__(1024) sandwich_sums_kernel(const SandwichGradP
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
   if (threadIdx.x != 0 || o >= p.cols) return;
-  if (blockIdx.y < 2) {
-    void *d = blockIdx.y ? p.dwp : p.dw;
-    if (p.w_f32)
-      static_cast<float *>(d)[o] = sum;
+  const auto value = [&](const void *w, bool f32) {
+    return f32 ? static_cast<const float *>(w)[o] : to_float(static_cast<const T *>(w)[o]);
+  };
+  const auto put = [&](void *d, bool f32, int64_t at, float v) {
+    if (f32)
+      static_cast<float *>(d)[at] = v;
     else
-      from_float(static_cast<T *>(d) + o, sum);
+      from_float(static_cast<T *>(d) + at, v);
+  };
+  if (blockIdx.y == 0) {
+    put(p.dw, p.w_f32, o, sum);
+  } else if (blockIdx.y == 1) {
+    if (p.dwp) put(p.dwp, p.w_f32, o, p.gate.p && one_gate(p) && p.rows > 0 ? value(p.gate.p, p.gate.f32) * sum : sum);
+    if (p.dgate && one_gate(p)) put(p.dgate, p.gate.f32, o, value(p.wp, p.w_f32) * sum);
   } else {
-    sum *= p.w_f32 ? static_cast<const float *>(p.wp)[o] : to_float(static_cast<const T *>(p.wp)[o]);
-    if (p.gate.f32)
-      static_cast<float *>(p.dgate)[group * p.lddgate + o] = sum;
-    else
-      from_float(static_cast<T *>(p.dgate) + group * p.lddgate + o, sum);
+    put(p.dgate, p.gate.f32, group * p.lddgate + o, value(p.wp, p.w_f32) * sum);
   }
 }
 
-template <class T, bool KA, bool KH>
+// How rows are laid over threads and CTAs: 512 threads an SM.
+struct RowsShape {
+  int threads, per_sm;
+  bool segments;
+  Split split;
+};
+RowsShape rows_shape(int64_t rows, int64_t cols, int sm_count) {
+  const int64_t chunks = (cols + 15) / 16;
+  RowsShape g;
+  g.segments = chunks > kMaxCluster * kClusterThreads;
+  unsigned cluster = 1;
+  while (!g.segments && chunks > cluster * kClusterThreads) cluster *= 2;
+  g.threads = g.segments ? kLongThreads : static_cast<int>(((chunks + cluster - 1) / cluster + 31) / 32 * 32);
+  g.per_sm = g.segments ? 1 : 512 / g.threads;
+  // (clusters of four and eight find room on all but four of a GB300's SMs, whatever the CTAs an SM: with one cluster for
+  // every four CTAs of all SMs the last ones ran by themselves, 8192 x 8192 with checkpoints 248 us)
+  const int64_t most = static_cast<int64_t>(cluster >= 4 && sm_count > 8 ? sm_count - 4 : sm_count) * g.per_sm / cluster;
+  const int64_t each = rows > 0 ? (rows + most - 1) / most : 1;
+  g.split = {static_cast<unsigned>((rows + each - 1) / each), static_cast<unsigned>(each), cluster};
+  return g;
+}
+// Rows in shared memory: as many as the SM's CTAs find room for, up to four.
+int rows_ahead(const RowsShape &g, int row_bytes) {
+  const int fit = kRowSmem / g.per_sm / row_bytes;
+  return fit < 1 ? 1 : fit < 4 ? fit : 4;
+}
+// Once for each kernel (each has its own Tag) and device: all the shared memory that a launch may ask for.
+template <class Tag, class F>
+cudaError_t allow_smem(F *kernel) {
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t set[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [dev, kernel] {
+    set[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
+  });
+  return set[dev];
+}
+
+template <class T, int KIND>
 cudaError_t rows_kernel(const SandwichGradParams &p, const RowsShape &g, uint32_t vec, cudaStream_t s) {
   struct Tag {};
-  const cudaError_t err = allow_smem<Tag>(sandwich_backward_kernel<T, KA, KH>);
+  const cudaError_t err = allow_smem<Tag>(sandwich_backward_kernel<T, KIND>);
   if (err != cudaSuccess) return err;
-  const int row_bytes = RowPlaces<T, KA, KH>::kBytes * g.threads, depth = rows_ahead(g, row_bytes);
-  return launch_maybe_pdl(sandwich_backward_kernel<T, KA, KH>, dim3(g.split.ctas), dim3(g.threads),
-                          static_cast<size_t>(depth) * row_bytes, s, true, p, g.split, depth, vec);
+  const int row_bytes = RowPlaces<T, KIND>::kBytes * g.threads, depth = rows_ahead(g, row_bytes);
+  return launch_cluster_maybe_pdl(sandwich_backward_kernel<T, KIND>, dim3(g.split.clusters * g.split.cluster),
+                                  dim3(g.threads), static_cast<size_t>(depth) * row_bytes, s, true,
+                                  static_cast<int>(g.split.cluster), p, g.split, depth, vec);
 }
 
 template <class T>
@@ -382,21 +549,23 @@ cudaError_t typed(const SandwichGradParams &p, cudaStream_t s, int *launches) {
   if (p.rows > 0) {
     cudaError_t err;
     if (g.segments)
-      err = launch_maybe_pdl(sandwich_backward_long_kernel<T>, dim3(g.split.ctas), dim3(g.threads), 0, s, true, p, g.split, vec);
-    else if (p.a.s)
-      err = p.h.s ? rows_kernel<T, true, true>(p, g, vec, s) : rows_kernel<T, true, false>(p, g, vec, s);
+      err = launch_maybe_pdl(sandwich_backward_long_kernel<T>, dim3(g.split.clusters), dim3(g.threads), 0, s, true, p, g.split, vec);
+    else if (!p.a.s != !p.h.s || p.a.e5m2 != p.h.e5m2)
+      err = rows_kernel<T, 3>(p, g, vec, s);
+    else if (!p.a.s)
+      err = rows_kernel<T, 0>(p, g, vec, s);
     else
-      err = p.h.s ? rows_kernel<T, false, true>(p, g, vec, s) : rows_kernel<T, false, false>(p, g, vec, s);
+      err = p.a.e5m2 ? rows_kernel<T, 2>(p, g, vec, s) : rows_kernel<T, 1>(p, g, vec, s);
     if (err != cudaSuccess) return err;
     ++*launches;
   }
   if (!sums) return cudaSuccess;
   unsigned shared = 0;   // gate rows to be looked at
   bool by_group = false;
-  if (p.dgate && p.rows > 0 && g.split.rows % p.gate.rows != 0) {
+  if (p.dgate && p.rows > 0 && !one_gate(p) && g.split.rows % p.gate.rows != 0) {
     const int64_t groups = (p.rows + p.gate.rows - 1) / p.gate.rows;
-    by_group = groups < g.split.ctas;
-    shared = by_group ? static_cast<unsigned>(groups) : g.split.ctas - 1;
+    by_group = groups < g.split.clusters;
+    shared = by_group ? static_cast<unsigned>(groups) : g.split.clusters - 1;
   }
   ++*launches;
   return launch_maybe_pdl(sandwich_sums_kernel<T>, dim3(static_cast<unsigned>((p.cols + 31) / 32), 2 + shared),
@@ -406,7 +575,7 @@ cudaError_t typed(const SandwichGradParams &p, cudaStream_t s, int *launches) {
 }  // namespace
 
 int64_t sandwich_partials(int64_t rows, int64_t cols) {
-  return static_cast<int64_t>(rows_shape(rows, cols, kSms).split.ctas) * kParts * part_pitch(cols);
+  return static_cast<int64_t>(rows_shape(rows, cols, kSms).split.clusters) * kParts * part_pitch(cols);
 }
 
 cudaError_t launch_sandwich_norm_backward(const SandwichGradParams &p, cudaStream_t s, int *launches) {

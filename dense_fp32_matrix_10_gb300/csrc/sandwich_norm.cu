@@ -1,21 +1,23 @@
 // sandwich_norm.cu -- the norms around a block, with a quantised output.
+#include <type_traits>
+
 #include "sandwich_norm.cuh"
 
 namespace sg {
 namespace {
 
-// What a row's outputs need of 16 of its elements: a, h and the norm's factor of them.
+// What a row's outputs need of 16 of its elements.
 struct Outputs {
-  float2 a[8], h[8], y[8];
+  float2 na[8], h[8], y[8];   // -a, h, y
 };
 
 // Stores h, y quantised and, with KEEP, the checkpoints of a and h, and their blocks' scales.  KEEP: 0 none, 1 E4M3,
 // 2 E5M2.  c: the first element's column.  vec: 5 h, 6 q, 7 qa, 8 qh.
-template <class T, bool E5M2, int KEEP>
-__device__ __forceinline__ void store_outputs(const SandwichParams &p, int64_t row, int64_t c, int n, Outputs &o, uint32_t vec) {
+template <class T, bool E5M2, int KEEP, class C>
+__device__ __forceinline__ void store_outputs(const SandwichParams &p, int64_t row, C c, int n, Outputs &o, uint32_t vec) {
   const int lane8 = threadIdx.x & 7;
-  const int64_t block = c >> 7;
-  const bool live = block * 128 < p.cols;
+  const C block = c >> 7;
+  const bool live = static_cast<int64_t>(block) * 128 < p.cols;
   if (n < 16) {   // a row with a NaN or an infinity must not reach past its end
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -27,7 +29,7 @@ __device__ __forceinline__ void store_outputs(const SandwichParams &p, int64_t r
   float scale;
   int own = 0;
   if (KEEP) {
-    const float m[4] = {max_abs16(o.y), max_abs16(o.h), max_abs16(o.a), 0.0f};
+    const float m[4] = {max_abs16(o.y), max_abs16(o.h), max_abs16(o.na), 0.0f};
     own = owned_by(lane8);
     scale = scale_of(owned_max(m, lane8), own == 0 ? E5M2 : KEEP == 2);
   } else {
@@ -44,9 +46,7 @@ __device__ __forceinline__ void store_outputs(const SandwichParams &p, int64_t r
       if (lane8 == owner_of(1) && live) p.sh[row * p.ldsh + block] = scale;
     }
     if (p.qa) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o.a[i] = make_float2(-o.a[i].x, -o.a[i].y);
-      store16_fp8(p.qa + row * p.ldqa + c, quantise_exactly<KEEP == 2>(o.a, da, na), n, level(vec, 7));
+      store16_fp8(p.qa + row * p.ldqa + c, quantise_exactly<KEEP == 2>(o.na, da, na), n, level(vec, 7));
       if (lane8 == owner_of(2) && live) p.sa[row * p.ldsa + block] = scale;
     }
   }
@@ -72,148 +72,100 @@ __device__ __forceinline__ float square_sum(const float2 (&v)[8]) {
   return s.x + s.y;
 }
 
-// vec: 0 a, 1 x, 2 w, 3 wp, 4 gate, and see store_outputs
-template <class T, bool E5M2, int KEEP>
-__global__ void __launch_bounds__(kRowThreads, 1) sandwich_norm_kernel(const SandwichParams p, const Split split,
-                                                                       const int depth, const uint32_t vec) {
-  constexpr int U = sizeof(T);
-  extern __shared__ __align__(16) uint4 rows_smem[];   // [depth][a, x][U][thread]
-  __shared__ float red[2][16];
+// FORM: kWarps, a row a warp and eight rows a CTA; kOne, a row a CTA; kLong, rows of more than 16384 elements, in segments
+// of that many: a three times, x twice from memory (or the L2 cache).  (A row that is the same for the whole CTA is left to
+// the uniform data path, with its offsets.)  vec: 0 a, 1 x, 2 w, 3 wp, 4 gate, and see store_outputs
+enum : int { kWarps = 0, kOne = 1, kLong = 2 };
+template <class T, bool E5M2, int KEEP, int FORM>
+__global__ void __launch_bounds__(kRowThreads, 1) sandwich_norm_kernel(const SandwichParams p, const uint32_t vec) {
+  using Col = std::conditional_t<FORM == kLong, int64_t, int>;
+  __shared__ __align__(16) float red[2][1][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int step = blockDim.x;
-  const unsigned r0 = blockIdx.x * split.rows;
-  const unsigned r1 = static_cast<unsigned>(min(static_cast<int64_t>(r0) + split.rows, p.rows));
-  const int64_t c = threadIdx.x * 16;
-  const int n = static_cast<int>(max(int64_t(0), min(int64_t(16), p.cols - c)));
-  uint4 *mine = rows_smem + threadIdx.x;
-  const auto fetch = [&](unsigned row, int slot) {
-    if (row < r1) {
-      uint4 *to = mine + slot * 2 * U * step;
-      copy16(to, step, static_cast<const T *>(p.a) + row * p.lda + c, n, level(vec, 0));
-      copy16(to + U * step, step, static_cast<const T *>(p.x) + row * p.ldx + c, n, level(vec, 1));
-    }
-    copies_commit();
-  };
-  for (int d = 0; d < depth; ++d) fetch(r0 + d, d);
-  float2 w[8], m[8];
-  load16_w<T>(p.w, p.w_f32, c, n, level(vec, 2), w);
-  unsigned group = p.gate.p ? r0 / p.gate.rows : 0, group_end = p.gate.p ? (group + 1) * p.gate.rows : ~0u;
-  load_gated<T>(p.wp, p.w_f32, p.gate, group, c, n, level(vec, 3), level(vec, 4), m);
-  const float mean = 1.0f / static_cast<float>(p.cols);
-  int turn = 0, slot = 0;
-  for (unsigned row = r0; row < r1; ++row) {
-    if (row >= group_end) {
-      ++group;
-      group_end += p.gate.rows;
-      load_gated<T>(p.wp, p.w_f32, p.gate, group, c, n, level(vec, 3), level(vec, 4), m);
-    }
-    copies_wait(depth - 1);
-    Outputs o;
-    const uint4 *at = mine + slot * 2 * U * step;
-    unpack(take16<T>(at, step), o.a);
-    const Raw16<T> x = take16<T>(at + U * step, step);
-    fetch(row + depth, slot);
-    slot = slot + 1 == depth ? 0 : slot + 1;
-    const float tp = 1.0f / sqrtf(fmaf(row_total(square_sum(o.a), red, turn), mean, p.eps));
-    unpack(x, o.h);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o.h[i] = fma2(both(p.residual_scale), o.h[i], mul2(mul2(o.a[i], both(tp)), m[i]));
-    const float t = 1.0f / sqrtf(fmaf(row_total(square_sum(o.h), red, turn), mean, p.eps));
-    if (threadIdx.x == 0) {
-      if (p.tp) p.tp[row] = tp;
-      if (p.t) p.t[row] = t;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o.y[i] = mul2(mul2(o.h[i], both(t)), w[i]);
-    store_outputs<T, E5M2, KEEP>(p, row, c, n, o, vec);
-  }
-  copies_wait(0);
-}
-
-// Rows of more than 8192 elements, in segments of that many: a three times, x twice from memory (or the L2 cache).
-template <class T, bool E5M2, int KEEP>
-__global__ void __launch_bounds__(kRowThreads, 1) sandwich_norm_long_kernel(const SandwichParams p, const uint32_t vec) {
-  __shared__ float red[2][16];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t row = blockIdx.x;
+  RowSums<1> row_sums(red);
+  const int64_t row = FORM == kWarps ? static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y : blockIdx.x;
+  if (FORM == kWarps && row >= p.rows) return;   // (whole warps)
   const unsigned group = p.gate.p ? static_cast<unsigned>(row) / p.gate.rows : 0;
   const T *a = static_cast<const T *>(p.a) + row * p.lda, *x = static_cast<const T *>(p.x) + row * p.ldx;
   const float mean = 1.0f / static_cast<float>(p.cols);
-  int turn = 0;
-  const auto count = [&](int64_t c) { return static_cast<int>(max(int64_t(0), min(int64_t(16), p.cols - c))); };
-  float sum = 0.0f;
-  for (int64_t c = threadIdx.x * 16; c < p.cols; c += kRowElements) {
+  const Col cols = static_cast<Col>(p.cols), end = FORM == kLong ? cols : 1;
+  const auto column = [&](Col base) { return base + static_cast<Col>(threadIdx.x) * 16; };
+  const auto count = [&](Col base) { return static_cast<int>(max(Col(0), min(Col(16), cols - column(base)))); };
+  // (-a: the exact quotients of its checkpoint want it so)
+  Raw16<T> ra = negated(load16(a + column(0), count(0), level(vec, 0))), rx = load16(x + column(0), count(0), level(vec, 1));
+  float sum[1] = {0.0f};
+  for (Col base = 0; base < end; base += kRowElements) {
+    if (FORM == kLong) ra = negated(load16(a + column(base), count(base), level(vec, 0)));
     float2 v[8];
-    unpack(load16(a + c, count(c), level(vec, 0)), v);
-    sum += square_sum(v);
+    unpack(ra, v);
+    sum[0] += square_sum(v);
   }
-  const float tp = 1.0f / sqrtf(fmaf(row_total(sum, red, turn), mean, p.eps));
-  const auto make_h = [&](int64_t c, Outputs &o) {
-    const int n = count(c);
-    float2 m[8];
-    unpack(load16(a + c, n, level(vec, 0)), o.a);
-    unpack(load16(x + c, n, level(vec, 1)), o.h);
-    load_gated<T>(p.wp, p.w_f32, p.gate, group, c, n, level(vec, 3), level(vec, 4), m);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o.h[i] = fma2(both(p.residual_scale), o.h[i], mul2(mul2(o.a[i], both(tp)), m[i]));
-  };
+  row_sums(sum);
+  const float tp = rsqrtf(fmaf(sum[0], mean, p.eps));
   Outputs o;
-  sum = 0.0f;
-  for (int64_t c = threadIdx.x * 16; c < p.cols; c += kRowElements) {
-    make_h(c, o);
-    sum += square_sum(o.h);
+  const auto make_h = [&](Col base) {
+    float2 m[8];
+    load_gated<T>(p.wp, p.w_f32, p.gate, group, column(base), count(base), level(vec, 3), level(vec, 4), m);
+    if (FORM == kLong) {
+      ra = negated(load16(a + column(base), count(base), level(vec, 0)));
+      rx = load16(x + column(base), count(base), level(vec, 1));
+    }
+    unpack(ra, o.na);
+    unpack(rx, o.h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.h[i] = fma2(both(p.residual_scale), o.h[i], mul2(mul2(o.na[i], both(-tp)), m[i]));
+  };
+  sum[0] = 0.0f;
+  for (Col base = 0; base < end; base += kRowElements) {
+    make_h(base);
+    sum[0] += square_sum(o.h);
   }
-  const float t = 1.0f / sqrtf(fmaf(row_total(sum, red, turn), mean, p.eps));
+  row_sums(sum);
+  const float t = rsqrtf(fmaf(sum[0], mean, p.eps));
   if (threadIdx.x == 0) {
     if (p.tp) p.tp[row] = tp;
     if (p.t) p.t[row] = t;
   }
-  for (int64_t base = 0; base < p.cols; base += kRowElements) {   // (whole warps: the blocks' lanes stay together)
-    const int64_t c = base + threadIdx.x * 16;
+  for (Col base = 0; base < end; base += kRowElements) {   // (whole warps: the blocks' lanes stay together)
+    if (FORM == kLong) make_h(base);
     float2 w[8];
-    make_h(c, o);
-    load16_w<T>(p.w, p.w_f32, c, count(c), level(vec, 2), w);
+    load16_w<T>(p.w, p.w_f32, column(base), count(base), level(vec, 2), w);
+    unpack(ra, o.na);
 #pragma unroll
     for (int i = 0; i < 8; ++i) o.y[i] = mul2(mul2(o.h[i], both(t)), w[i]);
-    store_outputs<T, E5M2, KEEP>(p, row, c, count(c), o, vec);
+    store_outputs<T, E5M2, KEEP>(p, row, column(base), count(base), o, vec);
   }
 }
 
 template <class T, bool E5M2, int KEEP>
-cudaError_t launch(const SandwichParams &p, int sm_count, cudaStream_t s) {
+cudaError_t launch(const SandwichParams &p, cudaStream_t s) {
   constexpr int e = sizeof(T);
   const int ew = p.w_f32 ? 4 : e, eg = p.gate.f32 ? 4 : e;
   const uint32_t vec = level_of(p.a, p.lda, e, 0) | level_of(p.x, p.ldx, e, 1) | level_of(p.w, 0, ew, 2) |
                        level_of(p.wp, 0, ew, 3) | level_of(p.gate.p, p.gate.ld, eg, 4) | level_of(p.h, p.ldh, e, 5) |
                        level_of(p.q, p.ldq, 1, 6) | level_of(p.qa, p.ldqa, 1, 7) | level_of(p.qh, p.ldqh, 1, 8);
-  const RowsShape g = rows_shape(p.rows, p.cols, sm_count);
-  if (g.segments)
-    return launch_maybe_pdl(sandwich_norm_long_kernel<T, E5M2, KEEP>, dim3(static_cast<unsigned>(p.rows)), dim3(kRowThreads),
-                            0, s, true, p, vec);
-  struct Tag {};
-  const cudaError_t err = allow_smem<Tag>(sandwich_norm_kernel<T, E5M2, KEEP>);
-  if (err != cudaSuccess) return err;
-  const int row_bytes = 2 * e * 16 * g.threads, depth = rows_ahead(g, row_bytes);
-  return launch_maybe_pdl(sandwich_norm_kernel<T, E5M2, KEEP>, dim3(g.split.ctas), dim3(g.threads),
-                          static_cast<size_t>(depth) * row_bytes, s, true, p, g.split, depth, vec);
+  const int threads = row_threads(p.cols), rows = threads == 32 ? 8 : 1;   // of a CTA
+  const dim3 grid(static_cast<unsigned>((p.rows + rows - 1) / rows)), block(threads, rows);
+  const auto kernel = threads == 32             ? sandwich_norm_kernel<T, E5M2, KEEP, kWarps>
+                      : p.cols <= kRowElements ? sandwich_norm_kernel<T, E5M2, KEEP, kOne>
+                                               : sandwich_norm_kernel<T, E5M2, KEEP, kLong>;
+  return launch_maybe_pdl(kernel, grid, block, 0, s, true, p, vec);
 }
 
 template <class T>
-cudaError_t typed(const SandwichParams &p, int sm_count, cudaStream_t s) {
-  if (!(p.qa || p.qh)) return p.e5m2 ? launch<T, true, 0>(p, sm_count, s) : launch<T, false, 0>(p, sm_count, s);
-  if (p.keep_e5m2) return p.e5m2 ? launch<T, true, 2>(p, sm_count, s) : launch<T, false, 2>(p, sm_count, s);
-  return p.e5m2 ? launch<T, true, 1>(p, sm_count, s) : launch<T, false, 1>(p, sm_count, s);
+cudaError_t typed(const SandwichParams &p, cudaStream_t s) {
+  if (!(p.qa || p.qh)) return p.e5m2 ? launch<T, true, 0>(p, s) : launch<T, false, 0>(p, s);
+  if (p.keep_e5m2) return p.e5m2 ? launch<T, true, 2>(p, s) : launch<T, false, 2>(p, s);
+  return p.e5m2 ? launch<T, true, 1>(p, s) : launch<T, false, 1>(p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_sandwich_norm(const SandwichParams &p, int sm_count, cudaStream_t s) {
+cudaError_t launch_sandwich_norm(const SandwichParams &p, cudaStream_t s) {
   switch (p.typeX) {
-    case SGEMM_TYPE_F32: return typed<float>(p, sm_count, s);
-    case SGEMM_TYPE_BF16: return typed<__nv_bfloat16>(p, sm_count, s);
-    default: return typed<__half>(p, sm_count, s);
+    case SGEMM_TYPE_F32: return typed<float>(p, s);
+    case SGEMM_TYPE_BF16: return typed<__nv_bfloat16>(p, s);
+    default: return typed<__half>(p, s);
   }
 }
 

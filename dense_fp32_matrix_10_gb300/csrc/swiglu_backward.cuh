@@ -25,10 +25,11 @@ constexpr int kUnitThreads = 512;
 template <class T, int SRC>
 struct UnitTile {
   static constexpr int kDy = sizeof(T), kG = SRC ? 1 : sizeof(T);   // 16-byte units of 16 elements
-  static constexpr int kUnits = kDy + 2 * kG;                       // of a row
-  static constexpr int kRaw = 2 * kUnits * kUnitThreads * 16, kScales = SRC ? 4 * kUnitThreads * 4 : 0;
+  static constexpr int kUnits = kDy + 2 * kG;                       // of a row's 16 elements
+  static constexpr int kMine = 2 * kUnits + (SRC ? 1 : 0);          // of a thread: two rows', and the scales of their g, u
+  static constexpr int kRaw = kMine * kUnitThreads * 16;
   static constexpr int kPart = 16 * 3 * 128 * 4, kInv = 3 * 128 * 4;
-  static constexpr int kBytes = kRaw + kScales + kPart + kInv;
+  static constexpr int kBytes = kRaw + kPart + kInv;
 };
 
 // vec: 0 dy, 1 g, 2 u, 3 qr, 4 qc, 5 qy
@@ -37,10 +38,10 @@ __global__ void __launch_bounds__(kUnitThreads, 1)
     swiglu_backward_kernel(const SwigluGradParams p, const unsigned tiles_c, const unsigned tiles, const uint32_t vec) {
   using Tile = UnitTile<T, SRC>;
   extern __shared__ __align__(16) unsigned char smem[];
-  uint4 *raw = reinterpret_cast<uint4 *>(smem) + threadIdx.x;                       // [2][kUnits][thread]
-  float *src_scale = reinterpret_cast<float *>(smem + Tile::kRaw) + threadIdx.x;    // [2][g, u][thread]
-  float *part = reinterpret_cast<float *>(smem + Tile::kRaw + Tile::kScales);       // [warp][dg, du, y][column] maxima
-  float *col_inv = reinterpret_cast<float *>(smem + Tile::kRaw + Tile::kScales + Tile::kPart);    // [3][column_place()] -1 / scale
+  uint4 *raw = reinterpret_cast<uint4 *>(smem) + first_unit(Tile::kMine);      // [2][dy, g, u]
+  float *src_scale = reinterpret_cast<float *>(raw + 2 * Tile::kUnits * kUnitStep);   // [2][g, u]
+  float *part = reinterpret_cast<float *>(smem + Tile::kRaw);                  // [warp][dg, du, y][column] maxima
+  float *col_inv = reinterpret_cast<float *>(smem + Tile::kRaw + Tile::kPart);    // [3][column_place()] -1 / scale
   griddep_wait();
   griddep_launch_dependents();
   const int lane8 = threadIdx.x & 7, row64 = threadIdx.x >> 3, warp = threadIdx.x >> 5;
@@ -56,26 +57,26 @@ __global__ void __launch_bounds__(kUnitThreads, 1)
     for (int i = 0; i < 2; ++i) {
       const int row = 64 * i + row64, m = row < rows ? n : 0;
       const auto matrix = [&](const void *base, int64_t ld, int lv, uint4 *to) {
-        copy16(to, kUnitThreads, static_cast<const T *>(base) + top * ld + left + row * ld + lane8 * 16, m, lv);
+        copy16(to, static_cast<const T *>(base) + top * ld + left + row * ld + lane8 * 16, m, lv);
       };
-      uint4 *to = raw + i * Tile::kUnits * kUnitThreads;
+      uint4 *to = raw + i * Tile::kUnits * kUnitStep;
       matrix(p.dy, p.lddy, level(vec, 0), to);
-      to += Tile::kDy * kUnitThreads;
+      to += Tile::kDy * kUnitStep;
       if constexpr (SRC != 0) {
         const auto kept = [&](const Kept &k, int lv, uint4 *place, float *scale) {
           copy16_kept(place, scale, static_cast<const unsigned char *>(k.p) + top * k.ld + left + row * k.ld + lane8 * 16,
                       k.s + top * k.lds + tc + row * k.lds, m, lv);
         };
-        kept(p.g, level(vec, 1), to, src_scale + 2 * i * kUnitThreads);
-        kept(p.u, level(vec, 2), to + kUnitThreads, src_scale + (2 * i + 1) * kUnitThreads);
+        kept(p.g, level(vec, 1), to, src_scale + 2 * i);
+        kept(p.u, level(vec, 2), to + kUnitStep, src_scale + 2 * i + 1);
       } else {
         matrix(p.g.p, p.g.ld, level(vec, 1), to);
-        matrix(p.u.p, p.u.ld, level(vec, 2), to + Tile::kDy * kUnitThreads);
+        matrix(p.u.p, p.u.ld, level(vec, 2), to + Tile::kDy * kUnitStep);
       }
     }
     copies_commit();
   };
-  const auto take = [&](const uint4 *at, float2 (&x)[8]) { unpack(take16<T>(at, kUnitThreads), x); };
+  const auto take = [&](const uint4 *at, float2 (&x)[8]) { unpack(take16<T>(at), x); };
   const auto take_kept = [&](const uint4 *at, float scale, float2 (&x)[8]) {
     unpack_fp8<SRC == 2>(*at, x);
 #pragma unroll
@@ -93,16 +94,16 @@ __global__ void __launch_bounds__(kUnitThreads, 1)
     copies_wait(0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint4 *at = raw + i * Tile::kUnits * kUnitThreads;
+      const uint4 *at = raw + i * Tile::kUnits * kUnitStep;
       float2 dy[8], g[8], u[8];
       take(at, dy);
-      at += Tile::kDy * kUnitThreads;
+      at += Tile::kDy * kUnitStep;
       if constexpr (SRC != 0) {
-        take_kept(at, src_scale[2 * i * kUnitThreads], g);
-        take_kept(at + kUnitThreads, src_scale[(2 * i + 1) * kUnitThreads], u);
+        take_kept(at, src_scale[2 * i], g);
+        take_kept(at + kUnitStep, src_scale[2 * i + 1], u);
       } else {
         take(at, g);
-        take(at + Tile::kDy * kUnitThreads, u);
+        take(at + Tile::kDy * kUnitStep, u);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
