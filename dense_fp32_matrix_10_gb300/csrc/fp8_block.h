@@ -36,7 +36,7 @@ struct SandwichParams {
   int typeX, w_f32, e5m2, keep_e5m2;
   float eps, residual_scale;
 };
-cudaError_t launch_sandwich_norm(const SandwichParams &p, cudaStream_t s);
+cudaError_t launch_sandwich_norm(const SandwichParams &p, int sm_count, cudaStream_t s);
 
 struct SandwichGradParams {
   const void *dy, *dh, *wp, *w;

@@ -75,7 +75,8 @@ sgemm_status_t sgemm_sandwich_norm_fp8(
   const sgemm_status_t st = check_ranges(r);
   if (st != SGEMM_SUCCESS) return st;
   sgemm_status_t why = SGEMM_SUCCESS;
-  if (!device_state(&why)) return why;
+  DeviceState *d = device_state(&why);
+  if (!d) return why;
   SandwichParams p = {};
   p.a = A;
   p.x = X;
@@ -108,7 +109,7 @@ sgemm_status_t sgemm_sandwich_norm_fp8(
   p.keep_e5m2 = typeKeep == SGEMM_TYPE_E5M2;
   p.eps = eps;
   p.residual_scale = residual_scale;
-  return queued(launch_sandwich_norm(p, reinterpret_cast<cudaStream_t>(stream)), 1);
+  return queued(launch_sandwich_norm(p, d->sm_count, reinterpret_cast<cudaStream_t>(stream)), 1);
 }
 
 size_t sgemm_sandwich_norm_backward_workspace(int64_t rows, int64_t cols) {

@@ -72,12 +72,17 @@ __device__ __forceinline__ float square_sum(const float2 (&v)[8]) {
   return s.x + s.y;
 }
 
+// A thread holds N times 16 consecutive elements of a row (or of a segment of it): one, with 64 registers, or two, with 80,
+// which divides a thread's fixed work (sums, offsets) by more elements and lets three rows of 8192 share an SM, but leaves
+// few rows less parallel.  One against two, in us: 8192 x 8192 bf16 with checkpoints 144 and 135, without 103 and 88; 4096 x
+// 4096 38.5 and 39.2, 27.5 and 25.9; 512 x 4096 5.6 and 7.8; 4096 x 8192 F32 110 and 138.
 // FORM: kWarps, a row a warp and eight rows a CTA; kOne, a row a CTA; kLong, rows of more than 16384 elements, in segments
 // of that many: a three times, x twice from memory (or the L2 cache).  (A row that is the same for the whole CTA is left to
 // the uniform data path, with its offsets.)  vec: 0 a, 1 x, 2 w, 3 wp, 4 gate, and see store_outputs
 enum : int { kWarps = 0, kOne = 1, kLong = 2 };
-template <class T, bool E5M2, int KEEP, int FORM>
-__global__ void __launch_bounds__(kRowThreads, 1) sandwich_norm_kernel(const SandwichParams p, const uint32_t vec) {
+template <class T, bool E5M2, int KEEP, int FORM, int N>
+__global__ void __launch_bounds__(N == 1 ? kRowThreads : kPairThreads, N == 1 ? 1 : 3)
+    sandwich_norm_kernel(const SandwichParams p, const uint32_t vec) {
   using Col = std::conditional_t<FORM == kLong, int64_t, int>;
   __shared__ __align__(16) float red[2][1][32];
   griddep_wait();
@@ -89,36 +94,49 @@ __global__ void __launch_bounds__(kRowThreads, 1) sandwich_norm_kernel(const San
   const T *a = static_cast<const T *>(p.a) + row * p.lda, *x = static_cast<const T *>(p.x) + row * p.ldx;
   const float mean = 1.0f / static_cast<float>(p.cols);
   const Col cols = static_cast<Col>(p.cols), end = FORM == kLong ? cols : 1;
-  const auto column = [&](Col base) { return base + static_cast<Col>(threadIdx.x) * 16; };
-  const auto count = [&](Col base) { return static_cast<int>(max(Col(0), min(Col(16), cols - column(base)))); };
-  // (-a: the exact quotients of its checkpoint want it so)
-  Raw16<T> ra = negated(load16(a + column(0), count(0), level(vec, 0))), rx = load16(x + column(0), count(0), level(vec, 1));
+  const auto column = [&](Col base, int j) { return base + (static_cast<Col>(threadIdx.x) + j * static_cast<Col>(blockDim.x)) * 16; };
+  const auto count = [&](Col base, int j) { return static_cast<int>(max(Col(0), min(Col(16), cols - column(base, j)))); };
+  Raw16<T> ra[N], rx[N];
+  const auto load = [&](Col base, bool with_x) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      ra[j] = load16(a + column(base, j), count(base, j), level(vec, 0));
+      if (with_x) rx[j] = load16(x + column(base, j), count(base, j), level(vec, 1));
+    }
+  };
+  load(0, true);
   float sum[1] = {0.0f};
   for (Col base = 0; base < end; base += kRowElements) {
-    if (FORM == kLong) ra = negated(load16(a + column(base), count(base), level(vec, 0)));
-    float2 v[8];
-    unpack(ra, v);
-    sum[0] += square_sum(v);
+    if (FORM == kLong) load(base, false);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float2 v[8];
+      ra[j] = negated(ra[j]);   // (the exact quotients of its checkpoint want -a)
+      unpack(ra[j], v);
+      sum[0] += square_sum(v);
+    }
   }
   row_sums(sum);
   const float tp = rsqrtf(fmaf(sum[0], mean, p.eps));
-  Outputs o;
+  float2 h[N][8];
   const auto make_h = [&](Col base) {
-    float2 m[8];
-    load_gated<T>(p.wp, p.w_f32, p.gate, group, column(base), count(base), level(vec, 3), level(vec, 4), m);
-    if (FORM == kLong) {
-      ra = negated(load16(a + column(base), count(base), level(vec, 0)));
-      rx = load16(x + column(base), count(base), level(vec, 1));
-    }
-    unpack(ra, o.na);
-    unpack(rx, o.h);
+    if (FORM == kLong) load(base, true);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o.h[i] = fma2(both(p.residual_scale), o.h[i], mul2(mul2(o.na[i], both(-tp)), m[i]));
+    for (int j = 0; j < N; ++j) {
+      float2 m[8], v[8];
+      load_gated<T>(p.wp, p.w_f32, p.gate, group, column(base, j), count(base, j), level(vec, 3), level(vec, 4), m);
+      if (FORM == kLong) ra[j] = negated(ra[j]);
+      unpack(ra[j], v);
+      unpack(rx[j], h[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = fma2(both(p.residual_scale), h[j][i], mul2(mul2(v[i], both(-tp)), m[i]));
+    }
   };
   sum[0] = 0.0f;
   for (Col base = 0; base < end; base += kRowElements) {
     make_h(base);
-    sum[0] += square_sum(o.h);
+#pragma unroll
+    for (int j = 0; j < N; ++j) sum[0] += square_sum(h[j]);
   }
   row_sums(sum);
   const float t = rsqrtf(fmaf(sum[0], mean, p.eps));
@@ -128,44 +146,57 @@ __global__ void __launch_bounds__(kRowThreads, 1) sandwich_norm_kernel(const San
   }
   for (Col base = 0; base < end; base += kRowElements) {   // (whole warps: the blocks' lanes stay together)
     if (FORM == kLong) make_h(base);
-    float2 w[8];
-    load16_w<T>(p.w, p.w_f32, column(base), count(base), level(vec, 2), w);
-    unpack(ra, o.na);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o.y[i] = mul2(mul2(o.h[i], both(t)), w[i]);
-    store_outputs<T, E5M2, KEEP>(p, row, column(base), count(base), o, vec);
+    for (int j = 0; j < N; ++j) {
+      Outputs o;
+      float2 w[8];
+      load16_w<T>(p.w, p.w_f32, column(base, j), count(base, j), level(vec, 2), w);
+      unpack(ra[j], o.na);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o.h[i] = h[j][i];
+        o.y[i] = mul2(mul2(h[j][i], both(t)), w[i]);
+      }
+      store_outputs<T, E5M2, KEEP>(p, row, column(base, j), count(base, j), o, vec);
+    }
   }
 }
 
 template <class T, bool E5M2, int KEEP>
-cudaError_t launch(const SandwichParams &p, cudaStream_t s) {
+cudaError_t launch(const SandwichParams &p, int sm_count, cudaStream_t s) {
   constexpr int e = sizeof(T);
   const int ew = p.w_f32 ? 4 : e, eg = p.gate.f32 ? 4 : e;
   const uint32_t vec = level_of(p.a, p.lda, e, 0) | level_of(p.x, p.ldx, e, 1) | level_of(p.w, 0, ew, 2) |
                        level_of(p.wp, 0, ew, 3) | level_of(p.gate.p, p.gate.ld, eg, 4) | level_of(p.h, p.ldh, e, 5) |
                        level_of(p.q, p.ldq, 1, 6) | level_of(p.qa, p.ldqa, 1, 7) | level_of(p.qh, p.ldqh, 1, 8);
+  const int64_t chunks = (p.cols + 15) / 16;
+  if constexpr (e == 2) {
+    if (p.cols > 4096 && p.cols <= 32 * kPairThreads && p.rows >= 8 * sm_count)
+      return launch_maybe_pdl(sandwich_norm_kernel<T, E5M2, KEEP, kOne, 2>, dim3(static_cast<unsigned>(p.rows)),
+                              dim3(static_cast<unsigned>((chunks + 63) / 64 * 32)), 0, s, true, p, vec);
+  }
   const int threads = row_threads(p.cols), rows = threads == 32 ? 8 : 1;   // of a CTA
   const dim3 grid(static_cast<unsigned>((p.rows + rows - 1) / rows)), block(threads, rows);
-  const auto kernel = threads == 32             ? sandwich_norm_kernel<T, E5M2, KEEP, kWarps>
-                      : p.cols <= kRowElements ? sandwich_norm_kernel<T, E5M2, KEEP, kOne>
-                                               : sandwich_norm_kernel<T, E5M2, KEEP, kLong>;
+  const auto kernel = threads == 32             ? sandwich_norm_kernel<T, E5M2, KEEP, kWarps, 1>
+                      : p.cols <= kRowElements ? sandwich_norm_kernel<T, E5M2, KEEP, kOne, 1>
+                                               : sandwich_norm_kernel<T, E5M2, KEEP, kLong, 1>;
   return launch_maybe_pdl(kernel, grid, block, 0, s, true, p, vec);
 }
 
 template <class T>
-cudaError_t typed(const SandwichParams &p, cudaStream_t s) {
-  if (!(p.qa || p.qh)) return p.e5m2 ? launch<T, true, 0>(p, s) : launch<T, false, 0>(p, s);
-  if (p.keep_e5m2) return p.e5m2 ? launch<T, true, 2>(p, s) : launch<T, false, 2>(p, s);
-  return p.e5m2 ? launch<T, true, 1>(p, s) : launch<T, false, 1>(p, s);
+cudaError_t typed(const SandwichParams &p, int sm_count, cudaStream_t s) {
+  if (!(p.qa || p.qh)) return p.e5m2 ? launch<T, true, 0>(p, sm_count, s) : launch<T, false, 0>(p, sm_count, s);
+  if (p.keep_e5m2) return p.e5m2 ? launch<T, true, 2>(p, sm_count, s) : launch<T, false, 2>(p, sm_count, s);
+  return p.e5m2 ? launch<T, true, 1>(p, sm_count, s) : launch<T, false, 1>(p, sm_count, s);
 }
 
 }  // namespace
 
-cudaError_t launch_sandwich_norm(const SandwichParams &p, cudaStream_t s) {
+cudaError_t launch_sandwich_norm(const SandwichParams &p, int sm_count, cudaStream_t s) {
   switch (p.typeX) {
-    case SGEMM_TYPE_F32: return typed<float>(p, s);
-    case SGEMM_TYPE_BF16: return typed<__nv_bfloat16>(p, s);
-    default: return typed<__half>(p, s);
+    case SGEMM_TYPE_F32: return typed<float>(p, sm_count, s);
+    case SGEMM_TYPE_BF16: return typed<__nv_bfloat16>(p, sm_count, s);
+    default: return typed<__half>(p, sm_count, s);
   }
 }
 

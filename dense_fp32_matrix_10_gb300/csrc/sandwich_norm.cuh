@@ -24,6 +24,7 @@
 namespace sg {
 
 constexpr int kRowThreads = 1024, kRowElements = 16 * kRowThreads;   // of a row, or of a segment of a longer one
+constexpr int kPairThreads = 256;                                    // of a row with twice 16 elements a thread
 
 // Sums of K values (1 or 4) over a row's threads, in a fixed order.  A lane passes on the half of its values that the
 // other lane of a pair will own, then half of the rest, until each owns one; the lanes that own the same one are joined
