@@ -3,10 +3,13 @@
 //
 // A row is 16 consecutive elements a thread, 128 threads a CTA and, where it
 // has more than 2048 elements, up to eight CTAs of a cluster.  A cluster takes
-// consecutive rows one after the other: the row's weights and the sums over
-// rows stay in registers (64 of a thread's 128), and a thread copies its own
-// elements of the next rows to places of its own in shared memory.  An SM's
-// CTAs belong to different rows, which are in different phases.
+// consecutive rows one after the other: a row's values and the sums over rows
+// stay in registers (96 of a thread's 128), the weights in places of the
+// thread's own in shared memory, where it also copies its elements of the next
+// row as soon as it has taken this one's.  An SM's four CTAs belong to different
+// rows, which are in different phases.  (With the weights in registers and every
+// row read and unpacked twice, 4095 x 8192 from checkpoints took 101 us, so 86;
+// two rows copied ahead 89.)
 //
 // The second mean is that of a sum which is linear in the first, so both come
 // from three sums over the row, taken together:
@@ -21,7 +24,6 @@ namespace {
 
 constexpr int kSms = 152;   // of a GB300: sizes the partial sums, whose number must not depend on the device
 constexpr int kClusterThreads = 128, kMaxCluster = 8;   // of a CTA; CTAs of a row
-constexpr int kRowSmem = 224 * 1024;                    // of an SM for the copied rows
 constexpr int kLongThreads = 512, kLongElements = 16 * kLongThreads;   // of a segment of a longer row
 
 // Clusters, each with `rows` consecutive rows (the last one fewer), and their CTAs.
@@ -233,17 +235,31 @@ __device__ __forceinline__ void finish(const SandwichGradParams &p, int64_t row,
 
 // KIND: a and h are 0 matrices of T, 1 checkpoints in E4M3, 2 in E5M2, 3 any of these, each its own.
 // vec: 0 dy, 1 dh, 2 w, 3 wp, 4 gate, 5 da, 6 dx, 7 a, 8 h, 9 dgate
+// Sixteen floats of this thread's own in shared memory.
+__device__ __forceinline__ void load_own(const float4 *at, float2 (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 u = at[k * kUnitStep];
+    v[2 * k] = make_float2(u.x, u.y);
+    v[2 * k + 1] = make_float2(u.z, u.w);
+  }
+}
+__device__ __forceinline__ void store_own(float4 *at, const float2 (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) at[k * kUnitStep] = make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
+}
+
 template <class T, int KIND>
-struct RowPlaces {
-  static constexpr int U = sizeof(T), K = KIND == 1 || KIND == 2 ? 1 : U;   // 16-byte units of sixteen elements
-  static constexpr int kDh = U, kA = 2 * U, kH = kA + K, kUnits = kH + K;
-  static constexpr int kBytes = kUnits * 16 + (KIND ? 8 : 0);               // of a thread, with its scales
+struct RowPlaces {   // 16-byte units of a thread: w, gate wp, and the next row's inputs
+  static constexpr int U = sizeof(T), K = KIND == 1 || KIND == 2 ? 1 : U;
+  static constexpr int kGated = 4, kDy = 8, kDh = kDy + U, kA = kDh + U, kH = kA + K, kUnits = kH + K;
+  static constexpr int kBytes = kUnits * 16 + 8;   // of a thread, with the scales of a and h
 };
 template <class T, int KIND>
 __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(const SandwichGradParams p, const Split split,
-                                                                           const int depth, const uint32_t vec) {
+                                                                           const uint32_t vec) {
   using At = RowPlaces<T, KIND>;
-  extern __shared__ __align__(16) uint4 rows_smem[];   // [depth][warp][dy, dh, a, h][lane], then [depth][a's, h's scale][thread]
+  extern __shared__ __align__(16) uint4 own_smem[];   // [warp][unit][lane], then [a's, h's scale][thread]
   __shared__ __align__(16) ClusterTotals shared;
   ClusterSums row_sums(&shared, split.cluster, p.wait_budget_ns, p.status);
   griddep_wait();
@@ -253,16 +269,14 @@ __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(c
   const unsigned r1 = static_cast<unsigned>(min(static_cast<int64_t>(r0) + split.rows, p.rows));
   const unsigned c = (row_sums.rank * blockDim.x + threadIdx.x) * 16;
   const int n = max(0, min(16, static_cast<int>(p.cols) - static_cast<int>(c)));
-  uint4 *mine = rows_smem + first_unit(At::kUnits);
-  const unsigned step = blockDim.x * At::kUnits;
-  float *scales = reinterpret_cast<float *>(rows_smem + depth * step) + threadIdx.x;
+  uint4 *mine = own_smem + first_unit(At::kUnits);
+  float4 *weights = reinterpret_cast<float4 *>(mine), *gated = weights + At::kGated * kUnitStep;
+  float *scales = reinterpret_cast<float *>(own_smem + blockDim.x * At::kUnits) + threadIdx.x;
   // Whether this thread's elements of every input are copied asynchronously in whole units.
   const bool fast = n == 16 && level(vec, 0) && (!p.dh || level(vec, 1)) &&
                     (KIND == 0 ? level(vec, 7) && level(vec, 8) : KIND < 3 && level(vec, 7) == 2 && level(vec, 8) == 2);
-  const auto fetch = [&](unsigned row, int slot) {
+  const auto fetch = [&](unsigned row) {
     if (row < r1) {
-      uint4 *to = mine + slot * step;
-      float *s = scales + slot * 2 * blockDim.x;
       const T *dy = static_cast<const T *>(p.dy) + row * p.lddy + c, *dh = static_cast<const T *>(p.dh) + row * p.lddh + c;
       const auto matrix = [&](const Kept &k, int n, int lv, uint4 *place, float *scale) {
         if (KIND == 3 ? k.s != nullptr : KIND != 0)
@@ -271,25 +285,23 @@ __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(c
           copy16(place, static_cast<const T *>(k.p) + row * k.ld + c, n, lv);
       };
       if (fast) {
-        copy16(to, dy, 16, 1);
-        if (p.dh) copy16(to + At::kDh * kUnitStep, dh, 16, 1);
-        matrix(p.a, 16, 2, to + At::kA * kUnitStep, s);
-        matrix(p.h, 16, 2, to + At::kH * kUnitStep, s + blockDim.x);
+        copy16(mine + At::kDy * kUnitStep, dy, 16, 1);
+        if (p.dh) copy16(mine + At::kDh * kUnitStep, dh, 16, 1);
+        matrix(p.a, 16, 2, mine + At::kA * kUnitStep, scales);
+        matrix(p.h, 16, 2, mine + At::kH * kUnitStep, scales + blockDim.x);
       } else {
-        copy16(to, dy, n, level(vec, 0));
-        if (p.dh) copy16(to + At::kDh * kUnitStep, dh, n, level(vec, 1));
-        matrix(p.a, n, level(vec, 7), to + At::kA * kUnitStep, s);
-        matrix(p.h, n, level(vec, 8), to + At::kH * kUnitStep, s + blockDim.x);
+        copy16(mine + At::kDy * kUnitStep, dy, n, level(vec, 0));
+        if (p.dh) copy16(mine + At::kDh * kUnitStep, dh, n, level(vec, 1));
+        matrix(p.a, n, level(vec, 7), mine + At::kA * kUnitStep, scales);
+        matrix(p.h, n, level(vec, 8), mine + At::kH * kUnitStep, scales + blockDim.x);
       }
     }
     copies_commit();
   };
-  const auto take = [&](int slot, Inputs &x) {
-    const uint4 *at = mine + slot * step;
-    const float *s = scales + slot * 2 * blockDim.x;
-    unpack(take16<T>(at), x.dy);
+  const auto take = [&](Inputs &x) {
+    unpack(take16<T>(mine + At::kDy * kUnitStep), x.dy);
     if (p.dh) {
-      unpack(take16<T>(at + At::kDh * kUnitStep), x.dh);
+      unpack(take16<T>(mine + At::kDh * kUnitStep), x.dh);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x.dh[i] = both(0.0f);
@@ -300,27 +312,35 @@ __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(c
       else
         unpack(take16<T>(place), v);
     };
-    matrix(p.a, at + At::kA * kUnitStep, s, x.a);
-    matrix(p.h, at + At::kH * kUnitStep, s + blockDim.x, x.h);
+    matrix(p.a, mine + At::kA * kUnitStep, scales, x.a);
+    matrix(p.h, mine + At::kH * kUnitStep, scales + blockDim.x, x.h);
   };
-  for (int d = 0; d < depth; ++d) fetch(r0 + d, d);
-  float2 w[8], m[8], sw[8], sn[8];
+  fetch(r0);
+  unsigned group = p.gate.p ? r0 / p.gate.rows : 0, group_end = p.gate.p ? (group + 1) * p.gate.rows : ~0u;
+  const auto load_weights = [&] {
+    float2 v[8];
+    load_gated<T>(p, group, c, n, vec, v);
+    store_own(gated, v);
+  };
+  load_weights();
+  float2 sw[8], sn[8];
+  load16_w<T>(p.w, p.w_f32, c, n, level(vec, 2), sw);
+  store_own(weights, sw);
 #pragma unroll
   for (int i = 0; i < 8; ++i) sw[i] = sn[i] = both(0.0f);
-  load16_w<T>(p.w, p.w_f32, c, n, level(vec, 2), w);
-  unsigned group = p.gate.p ? r0 / p.gate.rows : 0, group_end = p.gate.p ? (group + 1) * p.gate.rows : ~0u;
-  load_gated<T>(p, group, c, n, vec, m);
   const float mean = 1.0f / static_cast<float>(p.cols);
-  int slot = 0;
   bool first = true;
   float t_next = p.t[r0], tp_next = p.tp[r0];
   for (unsigned row = r0; row < r1; ++row) {
     if (row >= group_end) {
       ++group;
       group_end += p.gate.rows;
-      load_gated<T>(p, group, c, n, vec, m);
+      load_weights();
     }
-    copies_wait(depth - 1);
+    copies_wait(0);
+    Inputs x;
+    take(x);
+    fetch(row + 1);
     const float t = t_next, tp = tp_next;
     if (row + 1 < r1) {
       t_next = p.t[row + 1];
@@ -328,19 +348,19 @@ __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(c
     }
     float total[4] = {};
     {
-      Inputs x;
-      take(slot, x);
+      float2 w[8], m[8];
+      load_own(weights, w);
+      load_own(gated, m);
       add_sums(x, w, m, t, total[0], total[1], total[2]);
     }
     if (!row_sums(total)) break;
-    asm volatile("" ::: "memory");   // (read again: the row's values do not stay in registers meanwhile)
+    asm volatile("" ::: "memory");   // (the weights are read again, they do not stay in registers meanwhile)
     {
-      Inputs x;
-      take(slot, x);
+      float2 w[8], m[8];
+      load_own(weights, w);
+      load_own(gated, m);
       finish<T>(p, row, c, n, x, w, m, factors(t, tp, total[0], total[1], total[2], mean), sw, sn, vec);
     }
-    fetch(row + depth, slot);
-    slot = slot + 1 == depth ? 0 : slot + 1;
     if (p.partial && (row + 1 == r1 || row + 1 == group_end)) {
       if (n > 0) flush<T>(p, stream, group, r0, r1, c, n, sn, first, vec);
       first = false;
@@ -526,33 +546,22 @@ RowsShape rows_shape(int64_t rows, int64_t cols, int sm_count) {
   g.split = {static_cast<unsigned>((rows + each - 1) / each), static_cast<unsigned>(each), cluster};
   return g;
 }
-// Rows in shared memory: as many as the SM's CTAs find room for, up to four.
-int rows_ahead(const RowsShape &g, int row_bytes) {
-  const int fit = kRowSmem / g.per_sm / row_bytes;
-  return fit < 1 ? 1 : fit < 4 ? fit : 4;
-}
-// Once for each kernel (each has its own Tag) and device: all the shared memory that a launch may ask for.
-template <class Tag, class F>
-cudaError_t allow_smem(F *kernel) {
+
+template <class T, int KIND>
+cudaError_t rows_kernel(const SandwichGradParams &p, const RowsShape &g, uint32_t vec, cudaStream_t s) {
+  constexpr int bytes = RowPlaces<T, KIND>::kBytes;
   static std::once_flag once[kMaxDevices];
   static cudaError_t set[kMaxDevices];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  std::call_once(once[dev], [dev, kernel] {
-    set[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
+  std::call_once(once[dev], [dev] {
+    set[dev] = cudaFuncSetAttribute(sandwich_backward_kernel<T, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    RowPlaces<T, KIND>::kBytes * kClusterThreads);
   });
-  return set[dev];
-}
-
-template <class T, int KIND>
-cudaError_t rows_kernel(const SandwichGradParams &p, const RowsShape &g, uint32_t vec, cudaStream_t s) {
-  struct Tag {};
-  const cudaError_t err = allow_smem<Tag>(sandwich_backward_kernel<T, KIND>);
-  if (err != cudaSuccess) return err;
-  const int row_bytes = RowPlaces<T, KIND>::kBytes * g.threads, depth = rows_ahead(g, row_bytes);
+  if (set[dev] != cudaSuccess) return set[dev];
   return launch_cluster_maybe_pdl(sandwich_backward_kernel<T, KIND>, dim3(g.split.clusters * g.split.cluster),
-                                  dim3(g.threads), static_cast<size_t>(depth) * row_bytes, s, true,
-                                  static_cast<int>(g.split.cluster), p, g.split, depth, vec);
+                                  dim3(g.threads), static_cast<size_t>(bytes) * g.threads, s, true,
+                                  static_cast<int>(g.split.cluster), p, g.split, vec);
 }
 
 template <class T>
