@@ -89,8 +89,9 @@ def forward_bounds(a, x, wp, w, gate, rho, eps):
     return tp, h, Eh, t, et, y, Ey
 
 
-NORM_SHAPES = [(1, 1), (1, 128), (7, 5), (129, 127), (1, 4096), (300, 1000), (700, 520), (612, 1024), (40, 2100), (305, 4097),
-               (612, 8192), (5, 16384), (3, 16392)]
+# a row a warp; a row a CTA of up to 1024 threads; two chunks a thread (16-bit types from 1216 rows on); longer rows
+NORM_SHAPES = [(1, 1), (1, 128), (7, 5), (129, 127), (19, 512), (1, 4096), (300, 1000), (700, 520), (612, 1024), (40, 2100),
+               (305, 4097), (612, 8192), (1217, 4104), (1300, 8192), (5, 16384), (3, 16392), (2, 33000)]
 
 
 @gpu
@@ -175,16 +176,18 @@ def check_gradient(got, want):
         assert within(getattr(got, name), value, lim), name
 
 
-GRADIENT_SHAPES = [(1, 1), (1, 128), (7, 5), (129, 127), (1, 4096), (300, 1000), (2500, 250), (1300, 264), (612, 1032), (700, 2056),
-                   (305, 4097), (460, 8192), (5, 8200), (310, 8201)]
+# CTAs of one to four warps, clusters of one, two, four and eight, longer rows; one row a cluster and many
+GRADIENT_SHAPES = [(1, 1), (1, 128), (7, 5), (129, 127), (1, 4096), (300, 1000), (2500, 250), (2600, 264), (612, 1032), (700, 2048),
+                   (700, 2056), (305, 4097), (700, 4096), (460, 8192), (5, 8200), (310, 8201), (150, 16384), (4, 16392), (310, 16400)]
 
 
 @gpu
 @pytest.mark.parametrize("shape", GRADIENT_SHAPES)
 @pytest.mark.parametrize("dtype", FLOATS)
-@pytest.mark.parametrize("gate", ["none", "one", "each"])
-@pytest.mark.parametrize("keep", [None, E4M3])
+@pytest.mark.parametrize("gate,keep", [("none", "tensors"), ("one", "e4m3"), ("each", "e5m2"), ("one", "types"), ("each", "a"),
+                                       ("none", "h")])
 def test_norms_gradient(sg, shape, dtype, gate, keep):  # noqa: F811
+    """From the tensors, from checkpoints of one type or of two, and from one of each."""
     rows, cols = shape
     a, h = randn(shape, 21, dtype, 3.0), randn(shape, 22, dtype)
     dy, dh = randn(shape, 23, dtype), randn(shape, 24, dtype)
@@ -195,8 +198,10 @@ def test_norms_gradient(sg, shape, dtype, gate, keep):  # noqa: F811
     tp, t = (1 / (mean_square(v.float())[:, 0] + 1e-6).sqrt() for v in (a, h))
     if gate == "none":
         dh = None
-    A, H = (a, h) if keep is None else (sg.quantize_fp8(a, dtype=keep), sg.quantize_fp8(h, dtype=E5M2))
-    va, vh = (v.double() if keep is None else v[0].double() * spread(v[1], 1, B, rows, cols) for v in (A, H))
+    kept = {"e4m3": (E4M3, E4M3), "e5m2": (E5M2, E5M2), "types": (E4M3, E5M2), "a": (E4M3, None), "h": (None, E5M2),
+            "tensors": (None, None)}[keep]
+    A, H = (v if k is None else sg.quantize_fp8(v, dtype=k) for v, k in zip((a, h), kept))
+    va, vh = (v[0].double() * spread(v[1], 1, B, rows, cols) if isinstance(v, tuple) else v.double() for v in (A, H))
     got = sg.sandwich_norm_backward(dy, A, H, wp, w, tp, t, gate=g, residual_scale=0.5, dh=dh)
     assert got.da.dtype == got.dx.dtype == dtype and got.dweight.dtype == got.dpost_weight.dtype == w.dtype
     assert (got.dgate is None) == (g is None)
@@ -205,7 +210,7 @@ def test_norms_gradient(sg, shape, dtype, gate, keep):  # noqa: F811
 
 @gpu
 @pytest.mark.parametrize("groups,each", [(1, 3), (2, 1), (3, 7), (2, 800), (5, 611), (40, 33), (900, 2), (7, 152), (1300, 1)])
-@pytest.mark.parametrize("cols", [250, 4096, 8200])
+@pytest.mark.parametrize("cols", [250, 4096, 8200, 16400])
 def test_gradient_of_gates_of_runs(sg, groups, each, cols):  # noqa: F811
     """Runs that lie in one CTA's rows, that end inside them, and that span several."""
     shape, dtype = (groups * each, cols), torch.bfloat16
@@ -501,6 +506,19 @@ def test_unit_writes_its_outputs_only(sg):  # noqa: F811
         n = ref.shape[1]
         left = 0x55 if got.dtype == torch.uint8 else -5
         assert torch.equal(got[:, :n], ref.view(got.dtype)) and (got[:, n:] == left).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype,first", [(E4M3, 2.0 ** 0), (E5M2, 2.0 ** 0), (E4M3, 2.0 ** -118), (E5M2, 2.0 ** -111), (E4M3, 2.0 ** 127)])
+def test_scales_are_the_quotients_for_every_significand(sg, dtype, first):  # noqa: F811
+    """A block's scale is max|x| / F rounded to FP32, although it is not divided: all 2^23 significands of a binade, those
+    next to the least scale and of the largest numbers among them."""
+    x = (torch.arange(1 << 23, device="cuda", dtype=torch.int32) + torch.tensor(first).view(torch.int32).item()).view(torch.float32)
+    o = sg.swiglu_fp8(x[:, None], torch.zeros_like(x)[:, None], dtype=dtype, checkpoint=dtype)
+    want = (x.double() / FMAX[dtype]).float().clamp_min(2.0 ** -126)
+    assert torch.equal(o.gate8[1][:, 0], want)
+    q = sg.quantize_fp8(x[:, None], dtype=dtype)
+    assert same(o.gate8[0], q[0]) and same(o.gate8[1], q[1])
 
 
 # ---------------------------------------------------------------- kept rows as a weight gradient's operand
