@@ -313,23 +313,71 @@ struct Weights {
   }
 };
 
-// The checkpoints of two rows x cols matrices (not allocated for type < 0).
-struct Checkpoints {
-  at::Tensor q[2], s[2];
-  int64_t ld = 1, lds = 1;
-  void make(const Matrix &like, int type) {
-    if (type < 0) return;
-    lds = at_least_1(blocks(like.cols));
-    for (int i = 0; i < 2; ++i) {
-      q[i] = empty_fp8(like.rows, like.cols, like, fp8_scalar(type), ld);
-      s[i] = empty({like.rows, blocks(like.cols)}, like, at::kFloat);
-    }
+// Tensors that live and die together in one allocation: the caching allocator takes some 0.8 us of a tensor's 1 us.
+class Together {
+  at::Tensor base;
+  int64_t used = 0;
+
+ public:
+  static int64_t room(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+  Together(int64_t bytes, const Matrix &like) : base(empty({bytes}, like, at::kByte)) {}
+  at::Tensor take(int64_t rows, int64_t cols, int64_t ld, at::ScalarType type, bool vector = false) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(),
+                                                            c10::scalarTypeToTypeMeta(type));
+    c10::TensorImpl *impl = t.unsafeGetTensorImpl();
+    const int64_t e = static_cast<int64_t>(c10::elementSize(type));
+    impl->set_storage_offset(used / e);
+    if (vector)
+      impl->set_sizes_and_strides(at::IntArrayRef({cols}), at::IntArrayRef({1}));
+    else
+      impl->set_sizes_and_strides(at::IntArrayRef({rows, cols}), at::IntArrayRef({ld, 1}));
+    used += room(rows * ld * e);
+    return t;
   }
-  void *qp(int i) const { return q[i].defined() ? q[i].data_ptr() : nullptr; }
-  float *sp(int i) const { return s[i].defined() ? s[i].data_ptr<float>() : nullptr; }
-  PyObject *pair(int i) {
-    if (!q[i].defined()) Py_RETURN_NONE;
-    return Py_BuildValue("(NN)", wrap(std::move(q[i])), wrap(std::move(s[i])));
+};
+// An 8-bit matrix, with row stride ld, and its scales.
+struct Pair {
+  at::Tensor q, s;
+  void *qp = nullptr;
+  float *sp = nullptr;
+  int64_t ld = 1, lds = 1;
+  static int64_t room(int64_t rows, int64_t ld, int64_t s_rows, int64_t s_cols) {
+    return Together::room(rows * ld) + Together::room(s_rows * s_cols * 4);
+  }
+  // `with`: the allocation to take it from, else one of its own.
+  void make(int64_t rows, int64_t cols, int64_t row_stride, int64_t s_rows, int64_t s_cols, at::ScalarType type,
+            const Matrix &like, Together *with = nullptr) {
+    ld = row_stride;
+    lds = at_least_1(s_cols);
+    const auto from = [&](Together &t) {
+      q = t.take(rows, cols, ld, type);
+      s = t.take(s_rows, s_cols, s_cols, at::kFloat);
+    };
+    if (rows * cols == 0) {
+      q = at::Tensor(at::detail::empty_strided_cuda({rows, cols}, {ld, 1}, type, like.t->device()));
+      s = empty({s_rows, s_cols}, like, at::kFloat);
+    } else if (with) {
+      from(*with);
+    } else {
+      Together own(room(rows, ld, s_rows, s_cols), like);
+      from(own);
+    }
+    qp = q.data_ptr();
+    sp = s.data_ptr<float>();
+  }
+  // of 1 x 128 blocks, rows on 16-byte boundaries
+  static int64_t stride(const Matrix &like) { return at_least_1((like.cols + 15) / 16 * 16); }
+  static int64_t rows_room(const Matrix &like) { return room(like.rows, stride(like), like.rows, blocks(like.cols)); }
+  void rows_of(const Matrix &like, int type, Together *with = nullptr) {
+    make(like.rows, like.cols, stride(like), like.rows, blocks(like.cols), fp8_scalar(type), like, with);
+  }
+  // of 128 x 1 blocks
+  void cols_of(const Matrix &like, int type) {
+    make(like.rows, like.cols, stride(like), blocks(like.rows), like.cols, fp8_scalar(type), like);
+  }
+  PyObject *pair() {
+    if (!q.defined()) Py_RETURN_NONE;
+    return Py_BuildValue("(NN)", wrap(std::move(q)), wrap(std::move(s)));
   }
 };
 
@@ -349,23 +397,27 @@ PyObject *sandwich_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       PyErr_Clear();
       Py_RETURN_NONE;
     }
-    const int64_t kb = blocks(x.cols), ld = at_least_1(x.cols);
-    int64_t ldq;
-    at::Tensor q = empty_fp8(x.rows, x.cols, x, fp8_scalar(tq), ldq), s = empty({x.rows, kb}, x, at::kFloat);
+    Pair q, a8, h8;
+    q.rows_of(x, tq);
     at::Tensor h = empty({x.rows, x.cols}, x, x.type), tp, t;
-    if (training) {
-      tp = empty({x.rows}, x, at::kFloat);
-      t = empty({x.rows}, x, at::kFloat);
+    if (training || tk >= 0) {   // what the backward pass wants
+      Together kept((training ? 2 * Together::room(x.rows * 4) : 0) + (tk >= 0 ? 2 * Pair::rows_room(x) : 0), x);
+      if (training) {
+        tp = kept.take(1, x.rows, x.rows, at::kFloat, true);
+        t = kept.take(1, x.rows, x.rows, at::kFloat, true);
+      }
+      if (tk >= 0) {
+        a8.rows_of(x, tk, &kept);
+        h8.rows_of(x, tk, &kept);
+      }
     }
-    Checkpoints k;
-    k.make(x, tk);
     USUAL(queue(f_sandwich, x.rows, x.cols, static_cast<float>(eps), static_cast<float>(rho), x.p, x.ld, r.p, r.ld,
                 type_code(x.type), w.post->data_ptr(), w.pre->data_ptr(), w.type, gate.p, gate.ld, gate.type, gate.group,
-                h.data_ptr(), ld, q.data_ptr(), static_cast<sgemm_type_t>(tq), ldq, s.data_ptr<float>(), at_least_1(kb),
-                training ? tp.data_ptr<float>() : nullptr, training ? t.data_ptr<float>() : nullptr, k.qp(0), k.ld, k.sp(0),
-                k.lds, k.qp(1), k.ld, k.sp(1), k.lds, static_cast<sgemm_type_t>(tk), stream_of(x.dev)) == SGEMM_SUCCESS);
-    return Py_BuildValue("(NNNNNNN)", wrap(std::move(q)), wrap(std::move(s)), wrap(std::move(h)),
-                         wrap_or_none(std::move(tp)), wrap_or_none(std::move(t)), k.pair(0), k.pair(1));
+                h.data_ptr(), at_least_1(x.cols), q.qp, static_cast<sgemm_type_t>(tq), q.ld, q.sp, q.lds,
+                training ? tp.data_ptr<float>() : nullptr, training ? t.data_ptr<float>() : nullptr, a8.qp, a8.ld, a8.sp,
+                a8.lds, h8.qp, h8.ld, h8.sp, h8.lds, static_cast<sgemm_type_t>(tk), stream_of(x.dev)) == SGEMM_SUCCESS);
+    return Py_BuildValue("(NNNNNNN)", wrap(std::move(q.q)), wrap(std::move(q.s)), wrap(std::move(h)),
+                         wrap_or_none(std::move(tp)), wrap_or_none(std::move(t)), a8.pair(), h8.pair());
   });
 }
 
@@ -389,8 +441,14 @@ PyObject *sandwich_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (a[9] != Py_None) USUAL(dh.set(a[9]) && dh.type == dy.type && fits(dh, dy.rows, dy.cols, dy.dev));
     const int64_t ld = at_least_1(dy.cols);
     at::Tensor da = empty({dy.rows, dy.cols}, dy, dy.type), dx = empty({dy.rows, dy.cols}, dy, dy.type);
-    at::Tensor dwp = empty({dy.cols}, dy, w.pre->scalar_type()), dw = empty({dy.cols}, dy, w.pre->scalar_type()), dg;
-    if (gate.t) dg = empty(gate.t->sizes(), dy, gate.t->scalar_type());
+    at::Tensor dwp, dw, dg;
+    {
+      Together vectors(3 * Together::room(dy.cols * 4), dy);
+      dwp = vectors.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
+      dw = vectors.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
+      if (gate.t) dg = gate.t->dim() == 1 ? vectors.take(1, dy.cols, dy.cols, gate.t->scalar_type(), true)
+                                          : empty(gate.t->sizes(), dy, gate.t->scalar_type());
+    }
     const size_t need = f_sandwich_workspace(dy.rows, dy.cols);
     at::Tensor ws = empty({static_cast<int64_t>(need / 4)}, dy, at::kFloat);
     USUAL(queue(f_sandwich_backward, dy.rows, dy.cols, static_cast<float>(rho), dy.p, dy.ld, dh.p, dh.ld, type_code(dy.type),
@@ -411,14 +469,17 @@ PyObject *swiglu(PyObject *, PyObject *const *a, Py_ssize_t n) {
     USUAL(n == 4 && g.set(a[0]) && u.set(a[1]) && float_type(g.type) >= 0 && u.type == g.type &&
           fits(u, g.rows, g.cols, g.dev) && current(g.dev));
     const int tq = static_cast<int>(PyLong_AsLong(a[2])), tk = static_cast<int>(PyLong_AsLong(a[3]));
-    int64_t ldq;
-    at::Tensor q = empty_fp8(g.rows, g.cols, g, fp8_scalar(tq), ldq), s = empty({g.rows, blocks(g.cols)}, g, at::kFloat);
-    Checkpoints k;
-    k.make(g, tk);
-    USUAL(queue(f_swiglu, g.rows, g.cols, g.p, g.ld, u.p, u.ld, type_code(g.type), q.data_ptr(),
-                static_cast<sgemm_type_t>(tq), ldq, s.data_ptr<float>(), at_least_1(blocks(g.cols)), k.qp(0), k.ld, k.sp(0),
-                k.lds, k.qp(1), k.ld, k.sp(1), k.lds, static_cast<sgemm_type_t>(tk), stream_of(g.dev)) == SGEMM_SUCCESS);
-    return Py_BuildValue("(NNNN)", wrap(std::move(q)), wrap(std::move(s)), k.pair(0), k.pair(1));
+    Pair q, g8, u8;
+    q.rows_of(g, tq);
+    if (tk >= 0) {
+      Together kept(2 * Pair::rows_room(g), g);
+      g8.rows_of(g, tk, &kept);
+      u8.rows_of(g, tk, &kept);
+    }
+    USUAL(queue(f_swiglu, g.rows, g.cols, g.p, g.ld, u.p, u.ld, type_code(g.type), q.qp, static_cast<sgemm_type_t>(tq), q.ld,
+                q.sp, q.lds, g8.qp, g8.ld, g8.sp, g8.lds, u8.qp, u8.ld, u8.sp, u8.lds, static_cast<sgemm_type_t>(tk),
+                stream_of(g.dev)) == SGEMM_SUCCESS);
+    return Py_BuildValue("(NNNN)", wrap(std::move(q.q)), wrap(std::move(q.s)), g8.pair(), u8.pair());
   });
 }
 
@@ -431,17 +492,16 @@ PyObject *swiglu_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
           current(dy.dev));
     const int tz = static_cast<int>(PyLong_AsLong(a[3])), ty = static_cast<int>(PyLong_AsLong(a[4]));
     const int64_t kb = blocks(dy.cols), rb = blocks(dy.rows), wide = 2 * kb * SGEMM_FP8_BLOCK, ld = at_least_1(wide);
-    int64_t ldy;
-    at::Tensor qr = empty({dy.rows, wide}, dy, fp8_scalar(tz)), qc = empty({dy.rows, wide}, dy, fp8_scalar(tz));
-    at::Tensor sr = empty({dy.rows, 2 * kb}, dy, at::kFloat), sc = empty({rb, wide}, dy, at::kFloat);
-    at::Tensor qy = empty_fp8(dy.rows, dy.cols, dy, fp8_scalar(ty), ldy), sy = empty({rb, dy.cols}, dy, at::kFloat);
+    Pair r, c, y;
+    r.make(dy.rows, wide, ld, dy.rows, 2 * kb, fp8_scalar(tz), dy);
+    c.make(dy.rows, wide, ld, rb, wide, fp8_scalar(tz), dy);
+    y.cols_of(dy, ty);
     USUAL(queue(f_swiglu_backward, dy.rows, dy.cols, dy.p, dy.ld, type_code(dy.type), G.m.p, type_code(G.m.type), G.m.ld,
                 G.scales(), G.s.ld, U.m.p, type_code(U.m.type), U.m.ld, U.scales(), U.s.ld, static_cast<sgemm_type_t>(tz),
-                qr.data_ptr(), ld, sr.data_ptr<float>(), at_least_1(2 * kb), qc.data_ptr(), ld, sc.data_ptr<float>(), ld,
-                static_cast<sgemm_type_t>(ty), qy.data_ptr(), ldy, sy.data_ptr<float>(), at_least_1(dy.cols),
+                r.qp, r.ld, r.sp, r.lds, c.qp, c.ld, c.sp, c.lds, static_cast<sgemm_type_t>(ty), y.qp, y.ld, y.sp, y.lds,
                 stream_of(dy.dev)) == SGEMM_SUCCESS);
-    return Py_BuildValue("(NNNNNN)", wrap(std::move(qr)), wrap(std::move(sr)), wrap(std::move(qc)), wrap(std::move(sc)),
-                         wrap(std::move(qy)), wrap(std::move(sy)));
+    return Py_BuildValue("(NNNNNN)", wrap(std::move(r.q)), wrap(std::move(r.s)), wrap(std::move(c.q)), wrap(std::move(c.s)),
+                         wrap(std::move(y.q)), wrap(std::move(y.s)));
   });
 }
 
@@ -452,12 +512,11 @@ PyObject *requantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
     USUAL(n == 3 && x.set(a[0]) && sx.set(a[1]) && fp8_type(x.type) >= 0 && sx.type == at::kFloat &&
           fits(sx, x.rows, blocks(x.cols), x.dev) && current(x.dev));
     const int tq = static_cast<int>(PyLong_AsLong(a[2]));
-    int64_t ldq;
-    at::Tensor q = empty_fp8(x.rows, x.cols, x, fp8_scalar(tq), ldq), s = empty({blocks(x.rows), x.cols}, x, at::kFloat);
-    USUAL(queue(f_requantize, x.rows, x.cols, x.p, type_code(x.type), x.ld, static_cast<const float *>(sx.p), sx.ld,
-                q.data_ptr(), static_cast<sgemm_type_t>(tq), ldq, s.data_ptr<float>(), at_least_1(x.cols),
-                stream_of(x.dev)) == SGEMM_SUCCESS);
-    return Py_BuildValue("(NN)", wrap(std::move(q)), wrap(std::move(s)));
+    Pair q;
+    q.cols_of(x, tq);
+    USUAL(queue(f_requantize, x.rows, x.cols, x.p, type_code(x.type), x.ld, static_cast<const float *>(sx.p), sx.ld, q.qp,
+                static_cast<sgemm_type_t>(tq), q.ld, q.sp, q.lds, stream_of(x.dev)) == SGEMM_SUCCESS);
+    return q.pair();
   });
 }
 

@@ -7,14 +7,12 @@
 //   v  = H gate wp,  da = tp (v - a tp^2 mean(v a))
 //   dw = sum dy h t,  dwp = sum H gate a tp,  dgate = wp sum H a tp
 //
-// A row lies in the registers of one CTA, 16 consecutive elements a thread, and
-// 1024 threads an SM with 64 registers each belong to two rows of 8192
-// elements, more shorter ones or one longer one: while some of an SM's CTAs
-// wait for a sum, stores or loads, another computes.  (With 512 threads of 128
-// registers, weights and the gradient's sums in them and rows copied ahead
-// through shared memory, one CTA an SM had all its warps in one phase, and the
-// times of copies, arithmetic and stores added up: 8192 x 8192 with checkpoints
-// 43, 67 and 32 us, 142 in all.)  Rows of more than 16384 elements are walked in
+// Both take a row into registers once, 16 consecutive elements a thread, and
+// have an SM work on several rows: while some wait for a sum, stores or loads,
+// another computes.  (With rows copied ahead through shared memory and one CTA of
+// 512 threads an SM all its warps were in one phase, and the times of copies,
+// arithmetic and stores added up: norms of 8192 x 8192 with checkpoints 43, 67
+// and 32 us, 142 in all.)  Rows of more than 16384 elements are walked in
 // segments, several times.
 #pragma once
 

@@ -11,7 +11,9 @@ A checkpoint is a matrix in 8 bits as quantize_fp8 makes it in (1, 128) blocks, 
 pass had, they take it or its checkpoint.
 
 Tensors, streams and errors are as in module fp8: 2-D CUDA tensors with unit column stride and any row stride, every
-function runs on ``stream`` or torch's current stream and returns once its work is queued, nothing here computes.
+function runs on ``stream`` or torch's current stream and returns once its work is queued, nothing here computes.  An 8-bit
+matrix and its scales may share one allocation, and so may all that a call returns for the backward pass, or the vectors that it
+returns.
 """
 import collections
 import ctypes

@@ -327,6 +327,18 @@ def test_norms_write_their_outputs_only(sg):  # noqa: F811
                            (q, want.q, 0x55), (qa, want.a8[0], 0x55), (qh, want.h8[0], 0x55)):
         n = ref.shape[1]
         assert torch.equal(got[:, :n], ref.view(got.dtype)) and (got[:, n:] == left).all()
+    for k in range(2):   # one of the checkpoints and of the statistics alone
+        q1, s1, t1 = b(cols), f(kb), f(rows)[0]
+        one = [(q1.data_ptr(), cols + 3, s1.data_ptr(), kb + 3), (None, 0, None, 0)]
+        stat = [t1.data_ptr(), None]
+        sg.sgemm_sandwich_norm_fp8(rows, cols, 1e-6, 1.0, a.data_ptr(), cols, x.data_ptr(), cols, 0, wp.data_ptr(),
+                                   w.data_ptr(), 0, None, 0, 0, 0, h.data_ptr(), cols + 3, q.data_ptr(), 8, cols + 3,
+                                   s.data_ptr(), kb + 3, stat[k], stat[1 - k], *one[k], *one[1 - k], 8,
+                                   torch.cuda.current_stream().cuda_stream)
+        ref8, reft = (want.a8, want.post_rstd) if k == 0 else (want.h8, want.rstd)
+        assert torch.equal(q1[:, :cols], ref8[0].view(torch.uint8)) and torch.equal(s1[:, :kb], ref8[1])
+        assert torch.equal(t1[:rows], reft) and (t1[rows:] == -5).all() and (q1[:, cols:] == 0x55).all()
+        assert torch.equal(h[:, :cols], want.h) and torch.equal(q[:, :cols], want.q.view(torch.uint8))
     dy = randn((rows, cols), 85)
     ref = sg.sandwich_norm_backward(dy, a, x, wp, w, want.post_rstd, want.rstd)
     da, dx = f(cols), f(cols)
@@ -495,6 +507,13 @@ def test_unit_writes_its_outputs_only(sg):  # noqa: F811
     sg.sgemm_swiglu_fp8(rows, cols, g.data_ptr(), cols, u.data_ptr(), cols, 0, q.data_ptr(), 8, cols + 3, s.data_ptr(),
                         kb + 3, qg.data_ptr(), cols + 3, s_g.data_ptr(), kb + 3, qu.data_ptr(), cols + 3, su.data_ptr(),
                         kb + 3, 8, stream)
+    for k in range(2):   # one of the checkpoints alone
+        q1, s1 = b(cols), f(rows, kb)
+        one = [(q1.data_ptr(), cols + 3, s1.data_ptr(), kb + 3), (None, 0, None, 0)]
+        sg.sgemm_swiglu_fp8(rows, cols, g.data_ptr(), cols, u.data_ptr(), cols, 0, q.data_ptr(), 8, cols + 3, s.data_ptr(),
+                            kb + 3, *one[k], *one[1 - k], 8, stream)
+        ref8 = (want.gate8, want.up8)[k]
+        assert torch.equal(q1[:, :cols], ref8[0].view(torch.uint8)) and torch.equal(s1[:, :kb], ref8[1])
     d = sg.swiglu_backward_fp8(dy, g, u, dtype=E5M2)
     qr, qc, qy, sr, sc, sy = b(wide), b(wide), b(cols), f(rows, 2 * kb), f(2, wide), f(2, cols)
     sg.sgemm_swiglu_backward_fp8(rows, cols, dy.data_ptr(), cols, 0, g.data_ptr(), 0, cols, None, 0, u.data_ptr(), 0, cols,
@@ -677,6 +696,34 @@ def test_block_on_another_stream_and_in_graphs(sg):  # noqa: F811
             graph.replay()
             torch.cuda.synchronize()
             assert all(same(p, q) for p, q in zip(out, ref))
+
+
+@gpu
+@pytest.mark.parametrize("rows,cols", [(40, 3000), (700, 8192), (9, 16384), (3, 16400)])
+def test_rows_over_clusters_in_graphs_and_side_by_side(sg, rows, cols):  # noqa: F811
+    """The gradient of long rows: captured and replayed, on two streams at once, and again and again, the same bits."""
+    a, x, dy, dh = (randn((rows, cols), 191 + i, torch.bfloat16) for i in range(4))
+    wp, w, g = randn(cols, 195), randn(cols, 196), randn(cols, 197)
+    o = sg.sandwich_norm_fp8(a, x, wp, w, gate=g, training=True, checkpoint=E4M3)
+
+    def call(**kw):
+        return sg.sandwich_norm_backward(dy, o.a8, o.h8, wp, w, o.post_rstd, o.rstd, gate=g, dh=dh, **kw)
+    want = call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [call(stream=s) for _ in range(10) for s in streams]
+    torch.cuda.synchronize()
+    assert all(same(p, q) for r in got for p, q in zip(r, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [call() for _ in range(3)]
+    for _ in range(2):
+        for v in outs[-1]:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(same(p, q) for r in outs for p, q in zip(r, want))
+    assert sg.sgemm_last_device_status() == 0
 
 
 @gpu
