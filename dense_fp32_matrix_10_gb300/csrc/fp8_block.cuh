@@ -37,9 +37,45 @@ __device__ __forceinline__ void store_32(void *p, const uint4 *u) {
                "r"(u[0].w), "r"(u[1].x), "r"(u[1].y), "r"(u[1].z), "r"(u[1].w)
                : "memory");
 }
-// p[0 .. n-1] (zeros beyond, nothing read there).
+// Whether the 16-byte units around the elements c .. c + 15 of a row lie in it whatever its alignment (c: a multiple of 16).
+template <class C>
+__device__ __forceinline__ bool inside(C c, C cols) { return c >= 16 && c + 24 <= cols; }
+// Sixteen elements off 16 bytes, from the aligned units around them: their 32-bit words moved down by up to three, then
+// their bytes.  (Rows of 4001 of 4000 x 4001 bf16, loaded so and element by element: norms with checkpoints 70 and 139 us,
+// their gradient 89 and 231, the unit 32 and 43, its gradient 54 and 58; rows of 4000: 44, 59, 28 and 46.)
 template <class T>
-__device__ __forceinline__ Raw16<T> load16(const T *p, int n, int level) {
+__device__ __forceinline__ Raw16<T> load16_across(const T *p) {
+  constexpr int W = 4 * static_cast<int>(sizeof(T));   // words
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint4 *from = reinterpret_cast<const uint4 *>(at & ~static_cast<uintptr_t>(15));
+  uint32_t w[W + 4];
+#pragma unroll
+  for (int i = 0; i < W / 4 + 1; ++i) {
+    const uint4 u = from[i];
+    w[4 * i] = u.x;
+    w[4 * i + 1] = u.y;
+    w[4 * i + 2] = u.z;
+    w[4 * i + 3] = u.w;
+  }
+  const bool two = at & 8, one = at & 4;
+#pragma unroll
+  for (int i = 0; i < W + 2; ++i) w[i] = two ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < W + 1; ++i) w[i] = one ? w[i + 1] : w[i];
+  if (sizeof(T) == 2) {
+    const int bits = static_cast<int>(at & 2) * 8;
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+  }
+  Raw16<T> r;
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i)
+    r.half[i / (sizeof(T) / 2)].u[i % (sizeof(T) / 2)] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  return r;
+}
+// p[0 .. n-1] (zeros beyond); nothing outside is read, but where `in` says that it is of the same row (see inside()).
+template <class T>
+__device__ __forceinline__ Raw16<T> load16(const T *p, int n, int level, bool in = false) {
   Raw16<T> r;
   if (n >= 16 && level == 2) {
     uint4 u[sizeof(T)];
@@ -47,6 +83,8 @@ __device__ __forceinline__ Raw16<T> load16(const T *p, int n, int level) {
     for (int i = 0; i < static_cast<int>(sizeof(T)); i += 2) load_32(u + i, reinterpret_cast<const uint4 *>(p) + i);
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) r.half[i / (sizeof(T) / 2)].u[i % (sizeof(T) / 2)] = u[i];
+  } else if (level == 0 && in) {
+    r = load16_across(p);
   } else {
     r.half[0] = load8(p, n, level);
     r.half[1] = load8(p + 8, n - 8, level);
@@ -197,13 +235,13 @@ __device__ __forceinline__ int first_unit(int units) {   // of this thread, wher
 }
 // Sixteen elements of T in sizeof(T) units.
 template <class T>
-__device__ __forceinline__ void copy16(uint4 *to, const T *x, int n, int level) {
+__device__ __forceinline__ void copy16(uint4 *to, const T *x, int n, int level, bool in = false) {
   constexpr int U = sizeof(T);
   if (n >= 16 && level) {
 #pragma unroll
     for (int k = 0; k < U; ++k) copy_16(to + k * kUnitStep, reinterpret_cast<const uint4 *>(x) + k);
   } else {
-    const Raw16<T> r = load16(x, n, level);
+    const Raw16<T> r = load16(x, n, level, in);
 #pragma unroll
     for (int k = 0; k < U; ++k) to[k * kUnitStep] = r.half[k / (U / 2)].u[k % (U / 2)];
   }

@@ -86,6 +86,11 @@ at::Tensor empty_fp8(int64_t rows, int64_t cols, const Matrix &like, at::ScalarT
   ld = at_least_1((cols + 15) / 16 * 16);
   return at::Tensor(at::detail::empty_strided_cuda({rows, cols}, {ld, 1}, type, like.t->device()));
 }
+// rows x cols elements, rows on 32-byte boundaries.
+at::Tensor empty_rows(const Matrix &like, int64_t &ld) {
+  ld = at_least_1((like.cols + 15) / 16 * 16);
+  return at::Tensor(at::detail::empty_strided_cuda({like.rows, like.cols}, {ld, 1}, like.type, like.t->device()));
+}
 // The block along the outer dimension that an operand's scales stand for (0: they do not fit).
 int scale_block(const Matrix &s, int64_t outer, int64_t kb, bool inner_rows) {
   if (s.type != at::kFloat) return 0;
@@ -399,7 +404,8 @@ PyObject *sandwich_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     Pair q, a8, h8;
     q.rows_of(x, tq);
-    at::Tensor h = empty({x.rows, x.cols}, x, x.type), tp, t;
+    int64_t ldh;
+    at::Tensor h = empty_rows(x, ldh), tp, t;
     if (training || tk >= 0) {   // what the backward pass wants
       Together kept((training ? 2 * Together::room(x.rows * 4) : 0) + (tk >= 0 ? 2 * Pair::rows_room(x) : 0), x);
       if (training) {
@@ -413,7 +419,7 @@ PyObject *sandwich_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     USUAL(queue(f_sandwich, x.rows, x.cols, static_cast<float>(eps), static_cast<float>(rho), x.p, x.ld, r.p, r.ld,
                 type_code(x.type), w.post->data_ptr(), w.pre->data_ptr(), w.type, gate.p, gate.ld, gate.type, gate.group,
-                h.data_ptr(), at_least_1(x.cols), q.qp, static_cast<sgemm_type_t>(tq), q.ld, q.sp, q.lds,
+                h.data_ptr(), ldh, q.qp, static_cast<sgemm_type_t>(tq), q.ld, q.sp, q.lds,
                 training ? tp.data_ptr<float>() : nullptr, training ? t.data_ptr<float>() : nullptr, a8.qp, a8.ld, a8.sp,
                 a8.lds, h8.qp, h8.ld, h8.sp, h8.lds, static_cast<sgemm_type_t>(tk), stream_of(x.dev)) == SGEMM_SUCCESS);
     return Py_BuildValue("(NNNNNNN)", wrap(std::move(q.q)), wrap(std::move(q.s)), wrap(std::move(h)),
@@ -439,8 +445,8 @@ PyObject *sandwich_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
       Py_RETURN_NONE;
     }
     if (a[9] != Py_None) USUAL(dh.set(a[9]) && dh.type == dy.type && fits(dh, dy.rows, dy.cols, dy.dev));
-    const int64_t ld = at_least_1(dy.cols);
-    at::Tensor da = empty({dy.rows, dy.cols}, dy, dy.type), dx = empty({dy.rows, dy.cols}, dy, dy.type);
+    int64_t ld;
+    at::Tensor da = empty_rows(dy, ld), dx = empty_rows(dy, ld);
     at::Tensor dwp, dw, dg;
     {
       Together vectors(3 * Together::room(dy.cols * 4), dy);
@@ -455,7 +461,7 @@ PyObject *sandwich_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 A.m.p, type_code(A.m.type), A.m.ld, A.scales(), A.s.ld, H.m.p, type_code(H.m.type), H.m.ld, H.scales(),
                 H.s.ld, w.post->data_ptr(), w.pre->data_ptr(), w.type, gate.p, gate.ld, gate.type, gate.group,
                 tp->data_ptr<float>(), t->data_ptr<float>(), da.data_ptr(), ld, dx.data_ptr(), ld, dwp.data_ptr(),
-                dw.data_ptr(), dg.defined() ? dg.data_ptr() : nullptr, ld, ws.data_ptr(), need,
+                dw.data_ptr(), dg.defined() ? dg.data_ptr() : nullptr, at_least_1(dy.cols), ws.data_ptr(), need,
                 stream_of(dy.dev)) == SGEMM_SUCCESS);
     return Py_BuildValue("(NNNNN)", wrap(std::move(da)), wrap(std::move(dx)), wrap(std::move(dwp)), wrap(std::move(dw)),
                          wrap_or_none(std::move(dg)));

@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(c
   uint4 *mine = own_smem + first_unit(At::kUnits);
   float4 *weights = reinterpret_cast<float4 *>(mine), *gated = weights + At::kGated * kUnitStep;
   float *scales = reinterpret_cast<float *>(own_smem + blockDim.x * At::kUnits) + threadIdx.x;
+  const bool in = inside(static_cast<int>(c), static_cast<int>(p.cols));
   // Whether this thread's elements of every input are copied asynchronously in whole units.
   const bool fast = n == 16 && level(vec, 0) && (!p.dh || level(vec, 1)) &&
                     (KIND == 0 ? level(vec, 7) && level(vec, 8) : KIND < 3 && level(vec, 7) == 2 && level(vec, 8) == 2);
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(c
         if (KIND == 3 ? k.s != nullptr : KIND != 0)
           copy16_kept(place, scale, static_cast<const unsigned char *>(k.p) + row * k.ld + c, k.s + row * k.lds + (c >> 7), n, lv);
         else
-          copy16(place, static_cast<const T *>(k.p) + row * k.ld + c, n, lv);
+          copy16(place, static_cast<const T *>(k.p) + row * k.ld + c, n, lv, in);
       };
       if (fast) {
         copy16(mine + At::kDy * kUnitStep, dy, 16, 1);
@@ -290,8 +291,8 @@ __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(c
         matrix(p.a, 16, 2, mine + At::kA * kUnitStep, scales);
         matrix(p.h, 16, 2, mine + At::kH * kUnitStep, scales + blockDim.x);
       } else {
-        copy16(mine + At::kDy * kUnitStep, dy, n, level(vec, 0));
-        if (p.dh) copy16(mine + At::kDh * kUnitStep, dh, n, level(vec, 1));
+        copy16(mine + At::kDy * kUnitStep, dy, n, level(vec, 0), in);
+        if (p.dh) copy16(mine + At::kDh * kUnitStep, dh, n, level(vec, 1), in);
         matrix(p.a, n, level(vec, 7), mine + At::kA * kUnitStep, scales);
         matrix(p.h, n, level(vec, 8), mine + At::kH * kUnitStep, scales + blockDim.x);
       }
@@ -390,9 +391,10 @@ __global__ void __launch_bounds__(kLongThreads, 1) sandwich_backward_long_kernel
   float2 w[8], m[8];
   const auto load = [&](unsigned row, unsigned group, int64_t c) {
     const int n = static_cast<int>(min(int64_t(16), p.cols - c));
-    unpack(load16(static_cast<const T *>(p.dy) + row * p.lddy + c, n, level(vec, 0)), x.dy);
+    const bool in = inside(c, p.cols);
+    unpack(load16(static_cast<const T *>(p.dy) + row * p.lddy + c, n, level(vec, 0), in), x.dy);
     if (p.dh) {
-      unpack(load16(static_cast<const T *>(p.dh) + row * p.lddh + c, n, level(vec, 1)), x.dh);
+      unpack(load16(static_cast<const T *>(p.dh) + row * p.lddh + c, n, level(vec, 1), in), x.dh);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x.dh[i] = both(0.0f);
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kLongThreads, 1) sandwich_backward_long_kernel
         unpack_kept<3>(load16_fp8(static_cast<const unsigned char *>(k.p) + row * k.ld + c, n, lv), k.s[row * k.lds + (c >> 7)],
                     k.e5m2, v);
       else
-        unpack(load16(static_cast<const T *>(k.p) + row * k.ld + c, n, lv), v);
+        unpack(load16(static_cast<const T *>(k.p) + row * k.ld + c, n, lv, in), v);
     };
     matrix(p.a, level(vec, 7), x.a);
     matrix(p.h, level(vec, 8), x.h);

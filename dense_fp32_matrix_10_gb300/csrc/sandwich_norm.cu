@@ -100,8 +100,9 @@ __global__ void __launch_bounds__(N == 1 ? kRowThreads : kPairThreads, N == 1 ? 
   const auto load = [&](Col base, bool with_x) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      ra[j] = load16(a + column(base, j), count(base, j), level(vec, 0));
-      if (with_x) rx[j] = load16(x + column(base, j), count(base, j), level(vec, 1));
+      const Col c = column(base, j);
+      ra[j] = load16(a + c, count(base, j), level(vec, 0), inside(c, cols));
+      if (with_x) rx[j] = load16(x + c, count(base, j), level(vec, 1), inside(c, cols));
     }
   };
   load(0, true);

@@ -21,8 +21,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
   const int64_t c = static_cast<int64_t>(block) * 128 + lane8 * 16;
   const int n = unit < units ? static_cast<int>(max(int64_t(0), min(int64_t(16), p.cols - c))) : 0;
   // with checkpoints g and u have the other sign, which the exact quotients want
-  Raw16<T> rg = load16(static_cast<const T *>(p.g) + row * p.ldg + c, n, level(vec, 0));
-  Raw16<T> ru = load16(static_cast<const T *>(p.u) + row * p.ldu + c, n, level(vec, 1));
+  const bool in = n == 16 && inside(c, p.cols);
+  Raw16<T> rg = load16(static_cast<const T *>(p.g) + row * p.ldg + c, n, level(vec, 0), in);
+  Raw16<T> ru = load16(static_cast<const T *>(p.u) + row * p.ldu + c, n, level(vec, 1), in);
   if (KEEP) {
     rg = negated(rg);
     ru = negated(ru);

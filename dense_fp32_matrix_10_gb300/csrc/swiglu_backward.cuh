@@ -57,7 +57,8 @@ __global__ void __launch_bounds__(kUnitThreads, 1)
     for (int i = 0; i < 2; ++i) {
       const int row = 64 * i + row64, m = row < rows ? n : 0;
       const auto matrix = [&](const void *base, int64_t ld, int lv, uint4 *to) {
-        copy16(to, static_cast<const T *>(base) + top * ld + left + row * ld + lane8 * 16, m, lv);
+        copy16(to, static_cast<const T *>(base) + top * ld + left + row * ld + lane8 * 16, m, lv,
+               m == 16 && inside(left + lane8 * 16, p.cols));
       };
       uint4 *to = raw + i * Tile::kUnits * kUnitStep;
       matrix(p.dy, p.lddy, level(vec, 0), to);

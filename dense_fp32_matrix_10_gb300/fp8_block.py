@@ -11,7 +11,8 @@ A checkpoint is a matrix in 8 bits as quantize_fp8 makes it in (1, 128) blocks, 
 pass had, they take it or its checkpoint.
 
 Tensors, streams and errors are as in module fp8: 2-D CUDA tensors with unit column stride and any row stride, every
-function runs on ``stream`` or torch's current stream and returns once its work is queued, nothing here computes.  An 8-bit
+function runs on ``stream`` or torch's current stream and returns once its work is queued, nothing here computes.  The
+matrices made here have rows that start on 16-byte (8-bit) or 32-byte boundaries: a row stride rounded up to 16.  An 8-bit
 matrix and its scales may share one allocation, and so may all that a call returns for the backward pass, or the vectors that it
 returns.
 """
@@ -152,6 +153,12 @@ def _gate(gate, rows, cols, types):
     return p, ld, code, max(rows // groups, 1) if groups else 1, dev
 
 
+def _empty_rows(rows, cols, like):
+    """(tensor of like's type, ld): rows on 32-byte boundaries."""
+    ld = max((cols + 15) // 16 * 16, 1)
+    return torch.empty_strided((rows, cols), (ld, 1), dtype=like.dtype, device=like.device), ld
+
+
 def _checkpoint(rows, cols, dtype, dev):
     q, ld = _empty_fp8(rows, cols, dtype, dev)
     return (q, torch.empty((rows, _cdiv(cols, BLOCK)), dtype=torch.float32, device=dev)), ld
@@ -189,9 +196,9 @@ def sandwich_norm_fp8(a, x, post_weight, weight, gate=None, residual_scale=1.0, 
         with ctx:
             return sandwich_norm_fp8(a, x, post_weight, weight, gate, residual_scale, eps, dtype, training, checkpoint)
     q, ldq = _empty_fp8(rows, cols, dtype, a.device)
-    kb, ld = _cdiv(cols, BLOCK), cols or 1
+    kb = _cdiv(cols, BLOCK)
     s = torch.empty((rows, kb), dtype=torch.float32, device=a.device)
-    h = torch.empty((rows, cols), dtype=a.dtype, device=a.device)
+    h, ld = _empty_rows(rows, cols, a)
     tp = t = a8 = h8 = ptp = pt = None
     keep = [None, 1, None, 1] * 2
     if training:
@@ -236,8 +243,8 @@ def sandwich_norm_backward(dy, a, h, post_weight, weight, post_rstd, rstd, gate=
     if ctx is not None:
         with ctx:
             return sandwich_norm_backward(dy, a, h, post_weight, weight, post_rstd, rstd, gate, residual_scale, dh)
-    lib, ld = _lib or _library(), cols or 1
-    da, dx = (torch.empty((rows, cols), dtype=dy.dtype, device=dy.device) for _ in range(2))
+    lib = _lib or _library()
+    (da, ld), (dx, _) = (_empty_rows(rows, cols, dy) for _ in range(2))
     dwp, dw = (torch.empty((cols,), dtype=weight.dtype, device=dy.device) for _ in range(2))
     dg = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=dy.device)
     need = lib.sgemm_sandwich_norm_backward_workspace(rows, cols)
@@ -247,7 +254,7 @@ def sandwich_norm_backward(dy, a, h, post_weight, weight, post_rstd, rstd, gate=
     _raise("sgemm_sandwich_norm_backward", lib.sgemm_sandwich_norm_backward(
         rows, cols, residual_scale, pd, lddy, pdh, lddh, tx, pa, ta, lda, psa, ldsa, ph, th, ldh, psh, ldsh, pwp, pw, tw,
         pg, ldg, tg, group, ptp, pt, da.data_ptr(), ld, dx.data_ptr(), ld, dwp.data_ptr(), dw.data_ptr(),
-        dg.data_ptr() if dg is not None and rows else None, ld, ws.data_ptr(), need, _current_raw_stream(dev)))
+        dg.data_ptr() if dg is not None and rows else None, cols or 1, ws.data_ptr(), need, _current_raw_stream(dev)))
     return SandwichNormGrad(da, dx, dwp, dw, dg)
 
 
