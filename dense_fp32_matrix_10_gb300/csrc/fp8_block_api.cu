@@ -32,7 +32,13 @@ unsigned group_of(int64_t group_rows, int64_t rows) {
   return static_cast<unsigned>(group_rows < rows ? group_rows : rows);
 }
 
+// (The row stride of a single row says nothing about its alignment.)
+Gate gate_of(const void *p, int64_t ld, unsigned group, int64_t rows, sgemm_type_t type) {
+  return {p, group >= rows ? 0 : ld, group, p && type == SGEMM_TYPE_F32};
+}
+
 }  // namespace
+
 }  // namespace sg
 
 using namespace sg;
@@ -82,7 +88,7 @@ sgemm_status_t sgemm_sandwich_norm_fp8(
   p.x = X;
   p.wp = WP;
   p.w = W;
-  p.gate = {GATE, ldgate, group, GATE && typeGate == SGEMM_TYPE_F32};
+  p.gate = gate_of(GATE, ldgate, group, rows, typeGate);
   p.h = H;
   p.q = static_cast<unsigned char *>(Q);
   p.qa = static_cast<unsigned char *>(QA);
@@ -170,7 +176,7 @@ sgemm_status_t sgemm_sandwich_norm_backward(
   p.w = W;
   p.a = kept(A, typeA, lda, SA, ldsa);
   p.h = kept(H, typeH, ldh, SH, ldsh);
-  p.gate = {GATE, ldgate, group, GATE && typeGate == SGEMM_TYPE_F32};
+  p.gate = gate_of(GATE, ldgate, group, rows, typeGate);
   p.tp = TP;
   p.t = T;
   p.da = DA;
@@ -183,7 +189,7 @@ sgemm_status_t sgemm_sandwich_norm_backward(
   p.lddh = lddh;
   p.ldda = ldda;
   p.lddx = lddx;
-  p.lddgate = lddgate;
+  p.lddgate = group >= rows ? 0 : lddgate;
   p.rows = rows;
   p.cols = cols;
   p.typeX = typeX;

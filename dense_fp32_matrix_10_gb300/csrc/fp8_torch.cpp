@@ -87,9 +87,9 @@ at::Tensor empty_fp8(int64_t rows, int64_t cols, const Matrix &like, at::ScalarT
   return at::Tensor(at::detail::empty_strided_cuda({rows, cols}, {ld, 1}, type, like.t->device()));
 }
 // rows x cols elements, rows on 32-byte boundaries.
-at::Tensor empty_rows(const Matrix &like, int64_t &ld) {
+at::Tensor empty_rows(int64_t rows, const Matrix &like, at::ScalarType type, int64_t &ld) {
   ld = at_least_1((like.cols + 15) / 16 * 16);
-  return at::Tensor(at::detail::empty_strided_cuda({like.rows, like.cols}, {ld, 1}, like.type, like.t->device()));
+  return at::Tensor(at::detail::empty_strided_cuda({rows, like.cols}, {ld, 1}, type, like.t->device()));
 }
 // The block along the outer dimension that an operand's scales stand for (0: they do not fit).
 int scale_block(const Matrix &s, int64_t outer, int64_t kb, bool inner_rows) {
@@ -405,7 +405,7 @@ PyObject *sandwich_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Pair q, a8, h8;
     q.rows_of(x, tq);
     int64_t ldh;
-    at::Tensor h = empty_rows(x, ldh), tp, t;
+    at::Tensor h = empty_rows(x.rows, x, x.type, ldh), tp, t;
     if (training || tk >= 0) {   // what the backward pass wants
       Together kept((training ? 2 * Together::room(x.rows * 4) : 0) + (tk >= 0 ? 2 * Pair::rows_room(x) : 0), x);
       if (training) {
@@ -446,14 +446,14 @@ PyObject *sandwich_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     if (a[9] != Py_None) USUAL(dh.set(a[9]) && dh.type == dy.type && fits(dh, dy.rows, dy.cols, dy.dev));
     int64_t ld;
-    at::Tensor da = empty_rows(dy, ld), dx = empty_rows(dy, ld);
+    at::Tensor da = empty_rows(dy.rows, dy, dy.type, ld), dx = empty_rows(dy.rows, dy, dy.type, ld);
     at::Tensor dwp, dw, dg;
     {
       Together vectors(3 * Together::room(dy.cols * 4), dy);
       dwp = vectors.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
       dw = vectors.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
       if (gate.t) dg = gate.t->dim() == 1 ? vectors.take(1, dy.cols, dy.cols, gate.t->scalar_type(), true)
-                                          : empty(gate.t->sizes(), dy, gate.t->scalar_type());
+                                          : empty_rows(gate.t->sizes()[0], dy, gate.t->scalar_type(), ld);
     }
     const size_t need = f_sandwich_workspace(dy.rows, dy.cols);
     at::Tensor ws = empty({static_cast<int64_t>(need / 4)}, dy, at::kFloat);
@@ -461,7 +461,7 @@ PyObject *sandwich_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 A.m.p, type_code(A.m.type), A.m.ld, A.scales(), A.s.ld, H.m.p, type_code(H.m.type), H.m.ld, H.scales(),
                 H.s.ld, w.post->data_ptr(), w.pre->data_ptr(), w.type, gate.p, gate.ld, gate.type, gate.group,
                 tp->data_ptr<float>(), t->data_ptr<float>(), da.data_ptr(), ld, dx.data_ptr(), ld, dwp.data_ptr(),
-                dw.data_ptr(), dg.defined() ? dg.data_ptr() : nullptr, at_least_1(dy.cols), ws.data_ptr(), need,
+                dw.data_ptr(), dg.defined() ? dg.data_ptr() : nullptr, ld, ws.data_ptr(), need,
                 stream_of(dy.dev)) == SGEMM_SUCCESS);
     return Py_BuildValue("(NNNNN)", wrap(std::move(da)), wrap(std::move(dx)), wrap(std::move(dwp)), wrap(std::move(dw)),
                          wrap_or_none(std::move(dg)));

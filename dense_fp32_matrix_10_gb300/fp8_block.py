@@ -246,7 +246,9 @@ def sandwich_norm_backward(dy, a, h, post_weight, weight, post_rstd, rstd, gate=
     lib = _lib or _library()
     (da, ld), (dx, _) = (_empty_rows(rows, cols, dy) for _ in range(2))
     dwp, dw = (torch.empty((cols,), dtype=weight.dtype, device=dy.device) for _ in range(2))
-    dg = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=dy.device)
+    dg = None
+    if gate is not None:
+        dg = torch.empty_like(gate) if gate.dim() == 1 else _empty_rows(len(gate), cols, gate)[0]
     need = lib.sgemm_sandwich_norm_backward_workspace(rows, cols)
     ws = torch.empty((need // 4,), dtype=torch.float32, device=dy.device)
     if dg is not None and rows == 0:
@@ -254,7 +256,7 @@ def sandwich_norm_backward(dy, a, h, post_weight, weight, post_rstd, rstd, gate=
     _raise("sgemm_sandwich_norm_backward", lib.sgemm_sandwich_norm_backward(
         rows, cols, residual_scale, pd, lddy, pdh, lddh, tx, pa, ta, lda, psa, ldsa, ph, th, ldh, psh, ldsh, pwp, pw, tw,
         pg, ldg, tg, group, ptp, pt, da.data_ptr(), ld, dx.data_ptr(), ld, dwp.data_ptr(), dw.data_ptr(),
-        dg.data_ptr() if dg is not None and rows else None, cols or 1, ws.data_ptr(), need, _current_raw_stream(dev)))
+        dg.data_ptr() if dg is not None and rows else None, ld, ws.data_ptr(), need, _current_raw_stream(dev)))
     return SandwichNormGrad(da, dx, dwp, dw, dg)
 
 
