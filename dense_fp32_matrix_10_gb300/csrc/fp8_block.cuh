@@ -41,8 +41,8 @@ __device__ __forceinline__ void store_32(void *p, const uint4 *u) {
 template <class C>
 __device__ __forceinline__ bool inside(C c, C cols) { return c >= 16 && c + 24 <= cols; }
 // Sixteen elements off 16 bytes, from the aligned units around them: their 32-bit words moved down by up to three, then
-// their bytes.  (4000 x 4001 bf16, so and with the inputs and outputs element by element: norms with checkpoints 48 and 139
-// us, their gradient 89 and 231, the unit 32 and 43, its gradient 54 and 58; with rows of 4000 44, 59, 28 and 46.)
+// their bytes.  (4000 x 4001 bf16, so and with the inputs and outputs element by element: norms with checkpoints 47 and 139
+// us, their gradient 69 and 231, the unit 32 and 43, its gradient 52 and 58; with rows of 4000 38, 49, 25 and 45.)
 template <class T>
 __device__ __forceinline__ Raw16<T> load16_across(const T *p) {
   constexpr int W = 4 * static_cast<int>(sizeof(T));   // words
@@ -86,8 +86,9 @@ __device__ __forceinline__ Raw16<T> load16(const T *p, int n, int level, bool in
   } else if (level == 0 && in) {
     r = load16_across(p);
   } else {
-    r.half[0] = load8(p, n, level);
-    r.half[1] = load8(p + 8, n - 8, level);
+    // (lanes behind a row's end skip it: norms 4000 x 4000 bf16 with checkpoints 38 us, else 44)
+    r.half[0] = n > 0 ? load8(p, n, level) : Raw<T>();
+    r.half[1] = n > 8 ? load8(p + 8, n - 8, level) : Raw<T>();
   }
   return r;
 }
@@ -148,8 +149,8 @@ __device__ __forceinline__ void store16(T *p, const float2 (&v)[8], int n, int l
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)); i += 2) store_32(reinterpret_cast<uint4 *>(p) + i, u + i);
   } else {
-    store8(p, f[0], n, level);
-    store8(p + 8, f[1], n - 8, level);
+    if (n > 0) store8(p, f[0], n, level);
+    if (n > 8) store8(p + 8, f[1], n - 8, level);
   }
 }
 // Sixteen weights (or a gate's row) of F32 or T.
@@ -172,15 +173,15 @@ __device__ __forceinline__ uint2 load8_fp8(const unsigned char *p, int n, bool v
 }
 __device__ __forceinline__ uint4 load16_fp8(const unsigned char *p, int n, int level) {
   if (n >= 16 && level == 2) return *reinterpret_cast<const uint4 *>(p);
-  const uint2 a = load8_fp8(p, n, level), b = load8_fp8(p + 8, n - 8, level);
+  const uint2 a = n > 0 ? load8_fp8(p, n, level) : make_uint2(0, 0), b = n > 8 ? load8_fp8(p + 8, n - 8, level) : make_uint2(0, 0);
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 __device__ __forceinline__ void store16_fp8(unsigned char *p, uint4 u, int n, int level) {
   if (n >= 16 && level == 2) {
     *reinterpret_cast<uint4 *>(p) = u;
   } else {
-    store8_fp8(p, make_uint2(u.x, u.y), n, level);
-    store8_fp8(p + 8, make_uint2(u.z, u.w), n - 8, level);
+    if (n > 0) store8_fp8(p, make_uint2(u.x, u.y), n, level);
+    if (n > 8) store8_fp8(p + 8, make_uint2(u.z, u.w), n - 8, level);
   }
 }
 // (exact)
@@ -213,6 +214,10 @@ __device__ __forceinline__ uint4 to_fp8x16(const float2 (&v)[8]) {
 __device__ __forceinline__ void copy_16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+// The first `bytes` of them (0 .. 16), zeros behind.
+__device__ __forceinline__ void copy_16(void *dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void copy_4(void *dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -233,13 +238,24 @@ constexpr int kUnitStep = 32;
 __device__ __forceinline__ int first_unit(int units) {   // of this thread, where each has `units` of them
   return (threadIdx.x >> 5) * units * kUnitStep + (threadIdx.x & 31);
 }
-// Sixteen elements of T in sizeof(T) units.
+// The first n (1 .. 16) of sixteen elements of T on 16 bytes, zeros behind, in sizeof(T) units.
+template <class T>
+__device__ __forceinline__ void copy16_first(uint4 *to, const T *x, int n) {
+  constexpr int U = sizeof(T);
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+    copy_16(to + k * kUnitStep, reinterpret_cast<const uint4 *>(x) + k, k == 0 ? min(n * U, 16) : max(0, min(n * U - 16 * k, 16)));
+}
+// n of any count and alignment: a row's end is copied like the rest of it where it is aligned, without a wait (4000 x 4008
+// bf16, the norms' gradient: 49 us, element by element 65).
 template <class T>
 __device__ __forceinline__ void copy16(uint4 *to, const T *x, int n, int level, bool in = false) {
   constexpr int U = sizeof(T);
   if (n >= 16 && level) {
 #pragma unroll
     for (int k = 0; k < U; ++k) copy_16(to + k * kUnitStep, reinterpret_cast<const uint4 *>(x) + k);
+  } else if (n > 0 && level) {
+    copy16_first(to, x, n);
   } else {
     const Raw16<T> r = load16(x, n, level, in);
 #pragma unroll
@@ -258,6 +274,8 @@ __device__ __forceinline__ Raw16<T> take16(const uint4 *at) {
 __device__ __forceinline__ void copy16_kept(uint4 *to, float *scale, const unsigned char *x, const float *s, int n, int level) {
   if (n >= 16 && level == 2)
     copy_16(to, x);
+  else if (n > 0 && level == 2)
+    copy_16(to, x, n);
   else
     *to = load16_fp8(x, n, level);
   if (n > 0)

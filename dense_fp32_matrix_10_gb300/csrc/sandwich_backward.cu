@@ -273,28 +273,43 @@ __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(c
   float4 *weights = reinterpret_cast<float4 *>(mine), *gated = weights + At::kGated * kUnitStep;
   float *scales = reinterpret_cast<float *>(own_smem + blockDim.x * At::kUnits) + threadIdx.x;
   const bool in = inside(static_cast<int>(c), static_cast<int>(p.cols));
-  // Whether this thread's elements of every input are copied asynchronously in whole units.
-  const bool fast = n == 16 && level(vec, 0) && (!p.dh || level(vec, 1)) &&
+  // Whether the elements of every input are copied asynchronously.
+  const bool fast = level(vec, 0) && (!p.dh || level(vec, 1)) &&
                     (KIND == 0 ? level(vec, 7) && level(vec, 8) : KIND < 3 && level(vec, 7) == 2 && level(vec, 8) == 2);
+  if (n <= 0) {   // nothing is ever copied to these places
+    for (int i = At::kDy; i < At::kUnits; ++i) mine[i * kUnitStep] = make_uint4(0, 0, 0, 0);
+    scales[0] = scales[blockDim.x] = 0.0f;
+  }
   const auto fetch = [&](unsigned row) {
-    if (row < r1) {
+    if (row < r1 && n > 0) {
       const T *dy = static_cast<const T *>(p.dy) + row * p.lddy + c, *dh = static_cast<const T *>(p.dh) + row * p.lddh + c;
-      const auto matrix = [&](const Kept &k, int n, int lv, uint4 *place, float *scale) {
-        if (KIND == 3 ? k.s != nullptr : KIND != 0)
-          copy16_kept(place, scale, static_cast<const unsigned char *>(k.p) + row * k.ld + c, k.s + row * k.lds + (c >> 7), n, lv);
-        else
-          copy16(place, static_cast<const T *>(k.p) + row * k.ld + c, n, lv, in);
+      const auto aligned = [&](int n) {
+        const auto matrix = [&](const Kept &k, uint4 *place, float *scale) {
+          if (KIND == 0)
+            copy16(place, static_cast<const T *>(k.p) + row * k.ld + c, n, 1);
+          else
+            copy16_kept(place, scale, static_cast<const unsigned char *>(k.p) + row * k.ld + c, k.s + row * k.lds + (c >> 7), n, 2);
+        };
+        copy16(mine + At::kDy * kUnitStep, dy, n, 1);
+        if (p.dh) copy16(mine + At::kDh * kUnitStep, dh, n, 1);
+        matrix(p.a, mine + At::kA * kUnitStep, scales);
+        matrix(p.h, mine + At::kH * kUnitStep, scales + blockDim.x);
       };
-      if (fast) {
-        copy16(mine + At::kDy * kUnitStep, dy, 16, 1);
-        if (p.dh) copy16(mine + At::kDh * kUnitStep, dh, 16, 1);
-        matrix(p.a, 16, 2, mine + At::kA * kUnitStep, scales);
-        matrix(p.h, 16, 2, mine + At::kH * kUnitStep, scales + blockDim.x);
+      if (fast && n == 16) {
+        aligned(16);
+      } else if (fast) {
+        aligned(n);
       } else {
+        const auto matrix = [&](const Kept &k, int lv, uint4 *place, float *scale) {
+          if (KIND == 3 ? k.s != nullptr : KIND != 0)
+            copy16_kept(place, scale, static_cast<const unsigned char *>(k.p) + row * k.ld + c, k.s + row * k.lds + (c >> 7), n, lv);
+          else
+            copy16(place, static_cast<const T *>(k.p) + row * k.ld + c, n, lv, in);
+        };
         copy16(mine + At::kDy * kUnitStep, dy, n, level(vec, 0), in);
         if (p.dh) copy16(mine + At::kDh * kUnitStep, dh, n, level(vec, 1), in);
-        matrix(p.a, n, level(vec, 7), mine + At::kA * kUnitStep, scales);
-        matrix(p.h, n, level(vec, 8), mine + At::kH * kUnitStep, scales + blockDim.x);
+        matrix(p.a, level(vec, 7), mine + At::kA * kUnitStep, scales);
+        matrix(p.h, level(vec, 8), mine + At::kH * kUnitStep, scales + blockDim.x);
       }
     }
     copies_commit();
