@@ -74,8 +74,9 @@ __device__ __forceinline__ float square_sum(const float2 (&v)[8]) {
 
 // A thread holds N times 16 consecutive elements of a row (or of a segment of it): one, with 64 registers, or two, with 80,
 // which divides a thread's fixed work (sums, offsets) by more elements and lets three rows of 8192 share an SM, but leaves
-// few rows less parallel.  One against two, in us: 8192 x 8192 bf16 with checkpoints 144 and 135, without 103 and 88; 4096 x
-// 4096 38.5 and 39.2, 27.5 and 25.9; 512 x 4096 5.6 and 7.8; 4096 x 8192 F32 110 and 138.
+// few rows less parallel.  Up to 5120 columns three rows or more share an SM either way.  One against two, in us: 8192 x 8192
+// bf16 with checkpoints 144 and 135, without 103 and 88; 4072 x 6144 F16 62.5 and 54.8, 52.7 and 42.2; 4072 x 5120 47.6 and
+// 50.6, 39.4 and 39.1; 4072 x 4224 44.9 and 49.5, 37.3 and 38.2; 512 x 4096 5.6 and 7.8; 4096 x 8192 F32 118 and 138.
 // FORM: kWarps, a row a warp and eight rows a CTA; kOne, a row a CTA; kLong, rows of more than 16384 elements, in segments
 // of that many: a three times, x twice from memory (or the L2 cache).  (A row that is the same for the whole CTA is left to
 // the uniform data path, with its offsets.)  vec: 0 a, 1 x, 2 w, 3 wp, 4 gate, and see store_outputs
@@ -172,7 +173,7 @@ cudaError_t launch(const SandwichParams &p, int sm_count, cudaStream_t s) {
                        level_of(p.q, p.ldq, 1, 6) | level_of(p.qa, p.ldqa, 1, 7) | level_of(p.qh, p.ldqh, 1, 8);
   const int64_t chunks = (p.cols + 15) / 16;
   if constexpr (e == 2) {
-    if (p.cols > 4096 && p.cols <= 32 * kPairThreads && p.rows >= 8 * sm_count)
+    if (p.cols > 5120 && p.cols <= 32 * kPairThreads && p.rows >= 8 * sm_count)
       return launch_maybe_pdl(sandwich_norm_kernel<T, E5M2, KEEP, kOne, 2>, dim3(static_cast<unsigned>(p.rows)),
                               dim3(static_cast<unsigned>((chunks + 63) / 64 * 32)), 0, s, true, p, vec);
   }

@@ -91,7 +91,7 @@ def forward_bounds(a, x, wp, w, gate, rho, eps):
 
 # a row a warp; a row a CTA of up to 1024 threads; two chunks a thread (16-bit types from 1216 rows on); longer rows
 NORM_SHAPES = [(1, 1), (1, 128), (7, 5), (129, 127), (19, 512), (1, 4096), (300, 1000), (700, 520), (612, 1024), (40, 2100),
-               (305, 4097), (612, 8192), (1217, 4104), (1300, 8192), (5, 16384), (3, 16392), (2, 33000)]
+               (305, 4097), (612, 8192), (1217, 4104), (1217, 5128), (1300, 8192), (5, 16384), (3, 16392), (2, 33000)]
 
 
 @gpu
