@@ -33,10 +33,13 @@ struct SandwichParams {
   unsigned char *q, *qa, *qh;
   float *s, *sa, *sh, *tp, *t;
   int64_t lda, ldx, ldh, ldq, lds, ldqa, ldsa, ldqh, ldsh, rows, cols;
-  int typeX, w_f32, e5m2, keep_e5m2;
+  int w_f32, e5m2, keep_e5m2;
   float eps, residual_scale;
 };
-cudaError_t launch_sandwich_norm(const SandwichParams &p, int sm_count, cudaStream_t s);
+// (one for each type of a)
+cudaError_t launch_sandwich_norm_f32(const SandwichParams &p, int sm_count, cudaStream_t s);
+cudaError_t launch_sandwich_norm_bf16(const SandwichParams &p, int sm_count, cudaStream_t s);
+cudaError_t launch_sandwich_norm_f16(const SandwichParams &p, int sm_count, cudaStream_t s);
 
 struct SandwichGradParams {
   const void *dy, *dh, *wp, *w;
@@ -71,7 +74,7 @@ struct SwigluGradParams {
   unsigned char *qr, *qc, *qy;
   float *sr, *sc, *sy;
   int64_t lddy, ldqr, ldsr, ldqc, ldsc, ldqy, ldsy, rows, cols;
-  int typeX, z_e5m2, y_e5m2;
+  int z_e5m2, y_e5m2;
 };
 // (one for each type of dy)
 cudaError_t launch_swiglu_backward_f32(const SwigluGradParams &p, int sm_count, cudaStream_t s);

@@ -109,13 +109,15 @@ sgemm_status_t sgemm_sandwich_norm_fp8(
   p.ldsh = ldsh;
   p.rows = rows;
   p.cols = cols;
-  p.typeX = typeX;
   p.w_f32 = typeW == SGEMM_TYPE_F32;
   p.e5m2 = typeQ == SGEMM_TYPE_E5M2;
   p.keep_e5m2 = typeKeep == SGEMM_TYPE_E5M2;
   p.eps = eps;
   p.residual_scale = residual_scale;
-  return queued(launch_sandwich_norm(p, d->sm_count, reinterpret_cast<cudaStream_t>(stream)), 1);
+  const auto launch = typeX == SGEMM_TYPE_F32    ? launch_sandwich_norm_f32
+                      : typeX == SGEMM_TYPE_BF16 ? launch_sandwich_norm_bf16
+                                                 : launch_sandwich_norm_f16;
+  return queued(launch(p, d->sm_count, reinterpret_cast<cudaStream_t>(stream)), 1);
 }
 
 size_t sgemm_sandwich_norm_backward_workspace(int64_t rows, int64_t cols) {
@@ -297,7 +299,6 @@ sgemm_status_t sgemm_swiglu_backward_fp8(
   p.ldsy = ldsy;
   p.rows = rows;
   p.cols = cols;
-  p.typeX = typeX;
   p.z_e5m2 = typeZ == SGEMM_TYPE_E5M2;
   p.y_e5m2 = typeY == SGEMM_TYPE_E5M2;
   const auto launch = typeX == SGEMM_TYPE_F32    ? launch_swiglu_backward_f32

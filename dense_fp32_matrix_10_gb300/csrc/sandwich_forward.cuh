@@ -1,4 +1,6 @@
-// sandwich_norm.cu -- the norms around a block, with a quantised output.
+// sandwich_forward.cuh -- the norms around a block, with a quantised output: one instance of the file for each type.
+#pragma once
+
 #include <type_traits>
 
 #include "sandwich_norm.cuh"
@@ -185,21 +187,13 @@ cudaError_t launch(const SandwichParams &p, int sm_count, cudaStream_t s) {
   return launch_maybe_pdl(kernel, grid, block, 0, s, true, p, vec);
 }
 
+}  // namespace
+
 template <class T>
-cudaError_t typed(const SandwichParams &p, int sm_count, cudaStream_t s) {
+cudaError_t launch_norms(const SandwichParams &p, int sm_count, cudaStream_t s) {
   if (!(p.qa || p.qh)) return p.e5m2 ? launch<T, true, 0>(p, sm_count, s) : launch<T, false, 0>(p, sm_count, s);
   if (p.keep_e5m2) return p.e5m2 ? launch<T, true, 2>(p, sm_count, s) : launch<T, false, 2>(p, sm_count, s);
   return p.e5m2 ? launch<T, true, 1>(p, sm_count, s) : launch<T, false, 1>(p, sm_count, s);
-}
-
-}  // namespace
-
-cudaError_t launch_sandwich_norm(const SandwichParams &p, int sm_count, cudaStream_t s) {
-  switch (p.typeX) {
-    case SGEMM_TYPE_F32: return typed<float>(p, sm_count, s);
-    case SGEMM_TYPE_BF16: return typed<__nv_bfloat16>(p, sm_count, s);
-    default: return typed<__half>(p, sm_count, s);
-  }
 }
 
 }  // namespace sg
