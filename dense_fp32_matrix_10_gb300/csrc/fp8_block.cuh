@@ -243,8 +243,10 @@ template <class T>
 __device__ __forceinline__ void copy16_first(uint4 *to, const T *x, int n) {
   constexpr int U = sizeof(T);
 #pragma unroll
-  for (int k = 0; k < U; ++k)
-    copy_16(to + k * kUnitStep, reinterpret_cast<const uint4 *>(x) + k, k == 0 ? min(n * U, 16) : max(0, min(n * U - 16 * k, 16)));
+  for (int k = 0; k < U; ++k) {
+    const int bytes = max(0, min(n * U - 16 * k, 16));
+    copy_16(to + k * kUnitStep, reinterpret_cast<const uint4 *>(x) + (bytes ? k : 0), bytes);   // (no address behind the row)
+  }
 }
 // n of any count and alignment: a row's end is copied like the rest of it where it is aligned, without a wait (4000 x 4008
 // bf16, the norms' gradient: 49 us, element by element 65).

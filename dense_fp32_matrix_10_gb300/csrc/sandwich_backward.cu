@@ -8,7 +8,7 @@
 // thread's own in shared memory, where it also copies its elements of the next
 // row as soon as it has taken this one's.  An SM's four CTAs belong to different
 // rows, which are in different phases.  (With the weights in registers and every
-// row read and unpacked twice, 4095 x 8192 from checkpoints took 101 us, so 86;
+// row read and unpacked twice, 4095 x 8192 from checkpoints took 101 us, so 86, 3.9 TB/s;
 // two rows copied ahead 89.)
 //
 // The second mean is that of a sum which is linear in the first, so both come

@@ -767,6 +767,18 @@ def test_extension_leaves_the_unusual_to_python(lib):
 
 
 @gpu
+@pytest.mark.parametrize("cols", [1, 15, 333, 1024])
+def test_rows_made_for_a_caller_are_aligned(sg, cols):  # noqa: F811
+    """Any number of columns: the next call's vectors fit the rows that this one made."""
+    a, x, dy = (randn((6, cols), 231 + i, torch.bfloat16) for i in range(3))
+    w, g = randn(cols, 234), randn((3, cols), 235, torch.bfloat16)
+    o = sg.sandwich_norm_fp8(a, x, w, w, gate=g, training=True, checkpoint=E4M3)
+    d = sg.sandwich_norm_backward(dy, a, o.h, w, w, o.post_rstd, o.rstd, gate=g)
+    for v in (o.h, d.da, d.dx, d.dgate, o.q, o.a8[0], o.h8[0]):
+        assert v.stride() == (-(-cols // 16) * 16, 1) and v.data_ptr() % 32 == 0
+
+
+@gpu
 @pytest.mark.parametrize("shape", [(1, 128), (5, 0), (0, 7), (70, 333), (258, 1024)])
 def test_both_ways_through_python(sg, monkeypatch, shape):  # noqa: F811
     """The extension module and the general code hand over the same calls."""
