@@ -87,9 +87,9 @@ at::Tensor empty_fp8(int64_t rows, int64_t cols, const Matrix &like, at::ScalarT
   return at::Tensor(at::detail::empty_strided_cuda({rows, cols}, {ld, 1}, type, like.t->device()));
 }
 // rows x cols elements, rows on 32-byte boundaries.
-at::Tensor empty_rows(int64_t rows, const Matrix &like, at::ScalarType type, int64_t &ld) {
-  ld = at_least_1((like.cols + 15) / 16 * 16);
-  return at::Tensor(at::detail::empty_strided_cuda({rows, like.cols}, {ld, 1}, type, like.t->device()));
+int64_t row_stride(const Matrix &like) { return at_least_1((like.cols + 15) / 16 * 16); }
+at::Tensor empty_rows(int64_t rows, const Matrix &like, at::ScalarType type) {
+  return at::Tensor(at::detail::empty_strided_cuda({rows, like.cols}, {row_stride(like), 1}, type, like.t->device()));
 }
 // The block along the outer dimension that an operand's scales stand for (0: they do not fit).
 int scale_block(const Matrix &s, int64_t outer, int64_t kb, bool inner_rows) {
@@ -325,6 +325,10 @@ class Together {
 
  public:
   static int64_t room(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+  // Whether a call's tensors are that small (the allocator's small blocks) that all of them may live as long as the last one:
+  // above that, those that the backward pass keeps do not hold on to those that the next product uses up.  (Host time of 16 x
+  // 256: norms with checkpoints 8.3 us, else 10.2, their gradient 10.0 and 12.4, the unit's 6.6 and 8.3.)
+  static bool small(int64_t bytes) { return bytes <= (1 << 20); }
   Together(int64_t bytes, const Matrix &like) : base(empty({bytes}, like, at::kByte)) {}
   at::Tensor take(int64_t rows, int64_t cols, int64_t ld, at::ScalarType type, bool vector = false) {
     at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(),
@@ -340,6 +344,9 @@ class Together {
     return t;
   }
 };
+int64_t rows_room(int64_t rows, const Matrix &like, at::ScalarType type) {
+  return Together::room(rows * row_stride(like) * static_cast<int64_t>(c10::elementSize(type)));
+}
 // An 8-bit matrix, with row stride ld, and its scales.
 struct Pair {
   at::Tensor q, s;
@@ -371,14 +378,14 @@ struct Pair {
     sp = s.data_ptr<float>();
   }
   // of 1 x 128 blocks, rows on 16-byte boundaries
-  static int64_t stride(const Matrix &like) { return at_least_1((like.cols + 15) / 16 * 16); }
-  static int64_t rows_room(const Matrix &like) { return room(like.rows, stride(like), like.rows, blocks(like.cols)); }
+  static int64_t rows_room(const Matrix &like) { return room(like.rows, row_stride(like), like.rows, blocks(like.cols)); }
   void rows_of(const Matrix &like, int type, Together *with = nullptr) {
-    make(like.rows, like.cols, stride(like), like.rows, blocks(like.cols), fp8_scalar(type), like, with);
+    make(like.rows, like.cols, row_stride(like), like.rows, blocks(like.cols), fp8_scalar(type), like, with);
   }
   // of 128 x 1 blocks
-  void cols_of(const Matrix &like, int type) {
-    make(like.rows, like.cols, stride(like), blocks(like.rows), like.cols, fp8_scalar(type), like);
+  static int64_t cols_room(const Matrix &like) { return room(like.rows, row_stride(like), blocks(like.rows), like.cols); }
+  void cols_of(const Matrix &like, int type, Together *with = nullptr) {
+    make(like.rows, like.cols, row_stride(like), blocks(like.rows), like.cols, fp8_scalar(type), like, with);
   }
   PyObject *pair() {
     if (!q.defined()) Py_RETURN_NONE;
@@ -403,18 +410,31 @@ PyObject *sandwich_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       Py_RETURN_NONE;
     }
     Pair q, a8, h8;
-    q.rows_of(x, tq);
-    int64_t ldh;
-    at::Tensor h = empty_rows(x.rows, x, x.type, ldh), tp, t;
-    if (training || tk >= 0) {   // what the backward pass wants
-      Together kept((training ? 2 * Together::room(x.rows * 4) : 0) + (tk >= 0 ? 2 * Pair::rows_room(x) : 0), x);
+    const int64_t ldh = row_stride(x);
+    at::Tensor h, tp, t;
+    const auto kept = [&](Together &with) {   // what the backward pass wants
       if (training) {
-        tp = kept.take(1, x.rows, x.rows, at::kFloat, true);
-        t = kept.take(1, x.rows, x.rows, at::kFloat, true);
+        tp = with.take(1, x.rows, x.rows, at::kFloat, true);
+        t = with.take(1, x.rows, x.rows, at::kFloat, true);
       }
       if (tk >= 0) {
-        a8.rows_of(x, tk, &kept);
-        h8.rows_of(x, tk, &kept);
+        a8.rows_of(x, tk, &with);
+        h8.rows_of(x, tk, &with);
+      }
+    };
+    const int64_t kept_room = (training ? 2 * Together::room(x.rows * 4) : 0) + (tk >= 0 ? 2 * Pair::rows_room(x) : 0);
+    const int64_t all = kept_room + Pair::rows_room(x) + rows_room(x.rows, x, x.type);
+    if (Together::small(all)) {
+      Together with(all, x);
+      q.rows_of(x, tq, &with);
+      h = with.take(x.rows, x.cols, ldh, x.type);
+      kept(with);
+    } else {
+      q.rows_of(x, tq);
+      h = empty_rows(x.rows, x, x.type);
+      if (kept_room) {
+        Together with(kept_room, x);
+        kept(with);
       }
     }
     USUAL(queue(f_sandwich, x.rows, x.cols, static_cast<float>(eps), static_cast<float>(rho), x.p, x.ld, r.p, r.ld,
@@ -445,18 +465,23 @@ PyObject *sandwich_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
       Py_RETURN_NONE;
     }
     if (a[9] != Py_None) USUAL(dh.set(a[9]) && dh.type == dy.type && fits(dh, dy.rows, dy.cols, dy.dev));
-    int64_t ld;
-    at::Tensor da = empty_rows(dy.rows, dy, dy.type, ld), dx = empty_rows(dy.rows, dy, dy.type, ld);
-    at::Tensor dwp, dw, dg;
-    {
-      Together vectors(3 * Together::room(dy.cols * 4), dy);
-      dwp = vectors.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
-      dw = vectors.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
-      if (gate.t) dg = gate.t->dim() == 1 ? vectors.take(1, dy.cols, dy.cols, gate.t->scalar_type(), true)
-                                          : empty_rows(gate.t->sizes()[0], dy, gate.t->scalar_type(), ld);
-    }
+    const int64_t ld = row_stride(dy), rows = rows_room(dy.rows, dy, dy.type), vector = Together::room(dy.cols * 4);
     const size_t need = f_sandwich_workspace(dy.rows, dy.cols);
-    at::Tensor ws = empty({static_cast<int64_t>(need / 4)}, dy, at::kFloat);
+    const bool gates = gate.t && gate.t->dim() == 2;
+    const auto gate_type = gate.t ? gate.t->scalar_type() : at::kFloat;
+    const int64_t gate_rows = gates ? gate.t->sizes()[0] : 0;
+    const int64_t all = 2 * rows + 3 * vector + rows_room(gate_rows, dy, gate_type) + Together::room(static_cast<int64_t>(need));
+    const bool small = Together::small(all);
+    Together with(small ? all : 3 * vector, dy);
+    const auto matrix = [&](int64_t n, at::ScalarType type) {
+      return small ? with.take(n, dy.cols, ld, type) : empty_rows(n, dy, type);
+    };
+    at::Tensor da = matrix(dy.rows, dy.type), dx = matrix(dy.rows, dy.type), dg;
+    at::Tensor dwp = with.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
+    at::Tensor dw = with.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
+    if (gate.t) dg = gates ? matrix(gate_rows, gate_type) : with.take(1, dy.cols, dy.cols, gate_type, true);
+    const int64_t floats = static_cast<int64_t>(need / 4);
+    at::Tensor ws = small ? with.take(1, floats, floats, at::kFloat, true) : empty({floats}, dy, at::kFloat);
     USUAL(queue(f_sandwich_backward, dy.rows, dy.cols, static_cast<float>(rho), dy.p, dy.ld, dh.p, dh.ld, type_code(dy.type),
                 A.m.p, type_code(A.m.type), A.m.ld, A.scales(), A.s.ld, H.m.p, type_code(H.m.type), H.m.ld, H.scales(),
                 H.s.ld, w.post->data_ptr(), w.pre->data_ptr(), w.type, gate.p, gate.ld, gate.type, gate.group,
@@ -476,11 +501,13 @@ PyObject *swiglu(PyObject *, PyObject *const *a, Py_ssize_t n) {
           fits(u, g.rows, g.cols, g.dev) && current(g.dev));
     const int tq = static_cast<int>(PyLong_AsLong(a[2])), tk = static_cast<int>(PyLong_AsLong(a[3]));
     Pair q, g8, u8;
-    q.rows_of(g, tq);
+    const bool small = tk >= 0 && Together::small(3 * Pair::rows_room(g));
+    if (!small) q.rows_of(g, tq);
     if (tk >= 0) {
-      Together kept(2 * Pair::rows_room(g), g);
-      g8.rows_of(g, tk, &kept);
-      u8.rows_of(g, tk, &kept);
+      Together with((small ? 3 : 2) * Pair::rows_room(g), g);
+      if (small) q.rows_of(g, tq, &with);
+      g8.rows_of(g, tk, &with);
+      u8.rows_of(g, tk, &with);
     }
     USUAL(queue(f_swiglu, g.rows, g.cols, g.p, g.ld, u.p, u.ld, type_code(g.type), q.qp, static_cast<sgemm_type_t>(tq), q.ld,
                 q.sp, q.lds, g8.qp, g8.ld, g8.sp, g8.lds, u8.qp, u8.ld, u8.sp, u8.lds, static_cast<sgemm_type_t>(tk),
@@ -499,9 +526,18 @@ PyObject *swiglu_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int tz = static_cast<int>(PyLong_AsLong(a[3])), ty = static_cast<int>(PyLong_AsLong(a[4]));
     const int64_t kb = blocks(dy.cols), rb = blocks(dy.rows), wide = 2 * kb * SGEMM_FP8_BLOCK, ld = at_least_1(wide);
     Pair r, c, y;
-    r.make(dy.rows, wide, ld, dy.rows, 2 * kb, fp8_scalar(tz), dy);
-    c.make(dy.rows, wide, ld, rb, wide, fp8_scalar(tz), dy);
-    y.cols_of(dy, ty);
+    const int64_t all = Pair::room(dy.rows, ld, dy.rows, 2 * kb) + Pair::room(dy.rows, ld, rb, wide) + Pair::cols_room(dy);
+    const auto make = [&](Together *with) {
+      r.make(dy.rows, wide, ld, dy.rows, 2 * kb, fp8_scalar(tz), dy, with);
+      c.make(dy.rows, wide, ld, rb, wide, fp8_scalar(tz), dy, with);
+      y.cols_of(dy, ty, with);
+    };
+    if (Together::small(all)) {
+      Together with(all, dy);
+      make(&with);
+    } else {
+      make(nullptr);
+    }
     USUAL(queue(f_swiglu_backward, dy.rows, dy.cols, dy.p, dy.ld, type_code(dy.type), G.m.p, type_code(G.m.type), G.m.ld,
                 G.scales(), G.s.ld, U.m.p, type_code(U.m.type), U.m.ld, U.scales(), U.s.ld, static_cast<sgemm_type_t>(tz),
                 r.qp, r.ld, r.sp, r.lds, c.qp, c.ld, c.sp, c.lds, static_cast<sgemm_type_t>(ty), y.qp, y.ld, y.sp, y.lds,

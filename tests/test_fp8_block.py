@@ -779,6 +779,22 @@ def test_rows_made_for_a_caller_are_aligned(sg, cols):  # noqa: F811
 
 
 @gpu
+def test_kept_tensors_hold_no_others(sg):  # noqa: F811
+    """Beyond a megabyte, what outlives the next product does not share its operand's memory."""
+    a, x, dy = (randn((1024, 1030), 241 + i, torch.bfloat16) for i in range(3))
+    w = randn(1030, 244)
+    o = sg.sandwich_norm_fp8(a, x, w, w, training=True, checkpoint=E4M3)
+    u = sg.swiglu_fp8(a, x, checkpoint=E4M3)
+    d = sg.sandwich_norm_backward(dy, o.a8, o.h8, w, w, o.post_rstd, o.rstd)
+    place = lambda t: t.untyped_storage().data_ptr()   # noqa: E731
+    assert len({place(o.q), place(o.h), place(o.h8[0])}) == 3
+    assert place(o.h8[0]) == place(o.a8[0]) == place(o.rstd)
+    assert place(u.q) != place(u.gate8[0])
+    assert len({place(d.da), place(d.dx), place(d.dweight)}) == 3
+    assert d.dweight.untyped_storage().nbytes() <= 4 * 4 * 1280   # (no workspace)
+
+
+@gpu
 @pytest.mark.parametrize("shape", [(1, 128), (5, 0), (0, 7), (70, 333), (258, 1024)])
 def test_both_ways_through_python(sg, monkeypatch, shape):  # noqa: F811
     """The extension module and the general code hand over the same calls."""
