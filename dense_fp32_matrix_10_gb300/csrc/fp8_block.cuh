@@ -184,6 +184,11 @@ __device__ __forceinline__ void store16_fp8(unsigned char *p, uint4 u, int n, in
     if (n > 8) store8_fp8(p + 8, make_uint2(u.z, u.w), n - 8, level);
   }
 }
+// The first n of sixteen, zeros behind.
+__device__ __forceinline__ uint4 first16_fp8(uint4 u, int n) {
+  const auto word = [&](uint32_t w, int m) { return m >= 4 ? w : m > 0 ? w & ((1u << 8 * m) - 1) : 0u; };
+  return n >= 16 ? u : make_uint4(word(u.x, n), word(u.y, n - 4), word(u.z, n - 8), word(u.w, n - 12));
+}
 // (exact)
 template <bool E5M2>
 __device__ __forceinline__ float2 unpack_fp8x2(uint16_t two) {
@@ -310,6 +315,16 @@ __device__ __forceinline__ float rcp_approx(float a) {   // one unit in the last
   float d;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(a));
   return d;
+}
+
+// Zeros for the elements from n on, whatever a row that holds a NaN or an infinity has made of those behind its end.
+__device__ __forceinline__ void clear_from(float2 (&v)[8], int n) {
+  if (n >= 16) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (2 * i >= n) v[i].x = 0.0f;
+    if (2 * i + 1 >= n) v[i].y = 0.0f;
+  }
 }
 
 // ------------------------------------------------------------ scales and quotients

@@ -104,9 +104,10 @@ SGEMM_API sgemm_status_t sgemm_swiglu_fp8(int64_t rows, int64_t cols, const void
  *   du = dy * g * p,     dg = dy * u * p * (1 + g * (1 - p)),     y = g * p * u
  *
  * G and U are of typeX, or checkpoints with their scales SG and SU (NULL
- * otherwise); typeG and typeU are the same.  With wide = cols rounded up to a multiple of 128,
- * [dg | du] is a rows x 2 wide matrix: dg in the columns 0 .. cols - 1, du in
- * wide .. wide + cols - 1, zeros between.  It is quantised to typeZ in 1 x 128
+ * otherwise); typeG and typeU are the same.  With wide = cols rounded up to a
+ * multiple of 128, [dg | du] is a rows x 2 wide matrix: dg in the columns
+ * 0 .. cols - 1, du in wide .. wide + cols - 1, zeros behind each (zeros in QR
+ * and QC, too, whatever the inputs hold).  It is quantised to typeZ in 1 x 128
  * blocks (QR; SR is rows x 2 wide / 128) and in 128 x 1 blocks (QC; SC is
  * ceil(rows / 128) x 2 wide); y, for the weight gradient of the projection
  * that read it, to typeY in 128 x 1 blocks (QY; SY is ceil(rows / 128) x cols).

@@ -1,0 +1,37 @@
+"""Around a gated block's 8-bit products: what has to hold exactly, or nearer than the bounds of test_fp8_block.py let see.
+"""
+import pytest
+import torch
+
+from .test_fp8 import B, E4M3, E5M2, FLOATS, rng, sg, strided  # noqa: F401
+from .test_fp8_block import halves, randn
+
+gpu = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- behind a row's end
+@gpu
+@pytest.mark.parametrize("cols", [1, 15, 17, 141, 1013])
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("keep", [E4M3, E5M2])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_padding_is_zero_whatever_a_row_ends_on(sg, cols, dtype, keep, bad):  # noqa: F811
+    """A last block whose scale is NaN or infinite reaches the row's own columns, not the zeros behind them."""
+    rows = 200
+    g, u, dy = (randn((rows, cols), 301 + i) for i in range(3))
+    g[7, -1] = u[9, -1] = bad
+    u[150, -1] = bad
+    G, V = sg.quantize_fp8(g, dtype=keep), sg.quantize_fp8(u, dtype=keep)
+    assert not torch.isfinite(G[1][7, -1]) and not torch.isfinite(V[1][9, -1])
+    for odd in (False, True):
+        kept = [tuple(strided(t, 3, 1) for t in k) if odd else k for k in (G, V)]
+        o = sg.swiglu_backward_fp8(dy.to(dtype), *kept)
+        halves(o, cols)
+        wide = o.q_rows.shape[1] // 2
+        assert (o.scale_cols.view(2, 2, wide)[:, :, cols:] == 2.0 ** -126).all()
+        last = cols // B * B if cols % B else cols - B   # the last block's columns take in the bad rows, the others do not
+        assert not torch.isfinite(o.scale_cols[0, last:cols]).any() and torch.isfinite(o.scale_cols[0, :last]).all()
+        rows_bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+        rows_bad[[7, 9, 150]] = True
+        for at in (0, wide):
+            assert torch.isfinite(o.scale_rows[~rows_bad, at // B:(at + wide) // B]).all()
