@@ -193,6 +193,12 @@ __device__ __forceinline__ void unpack_kept(uint4 u, float scale, bool e5m2, flo
 struct Inputs {
   float2 dy[8], dh[8], a[8], h[8];
 };
+// An infinite scale of a checkpoint makes NaN of the zeros behind a row's end, which are not of the row's sums.
+__device__ __forceinline__ void clear_kept(Inputs &x, int n) {
+  if (n >= 16) return;
+  clear_from(x.a, n);
+  clear_from(x.h, n);
+}
 // A, P and R over them.
 __device__ __forceinline__ void add_sums(const Inputs &x, const float2 (&w)[8], const float2 (&m)[8], float t, float &A,
                                          float &P, float &R) {
@@ -330,6 +336,7 @@ __global__ void __launch_bounds__(kClusterThreads, 4) sandwich_backward_kernel(c
     };
     matrix(p.a, mine + At::kA * kUnitStep, scales, x.a);
     matrix(p.h, mine + At::kH * kUnitStep, scales + blockDim.x, x.h);
+    if (KIND != 0) clear_kept(x, n);
   };
   fetch(r0);
   unsigned group = p.gate.p ? r0 / p.gate.rows : 0, group_end = p.gate.p ? (group + 1) * p.gate.rows : ~0u;
@@ -423,6 +430,7 @@ __global__ void __launch_bounds__(kLongThreads, 1) sandwich_backward_long_kernel
     };
     matrix(p.a, level(vec, 7), x.a);
     matrix(p.h, level(vec, 8), x.h);
+    clear_kept(x, n);
     load16_w<T>(p.w, p.w_f32, c, n, level(vec, 2), w);
     load_gated<T>(p, group, c, n, vec, m);
     return n;

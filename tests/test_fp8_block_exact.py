@@ -35,3 +35,24 @@ def test_padding_is_zero_whatever_a_row_ends_on(sg, cols, dtype, keep, bad):  # 
         rows_bad[[7, 9, 150]] = True
         for at in (0, wide):
             assert torch.isfinite(o.scale_rows[~rows_bad, at // B:(at + wide) // B]).all()
+
+
+@gpu
+@pytest.mark.parametrize("cols", [5, 141, 2101, 16401])
+@pytest.mark.parametrize("dtype", FLOATS)
+def test_an_infinite_scale_at_a_rows_end_in_the_norms_gradient(sg, cols, dtype):  # noqa: F811
+    """h infinite in a row's last block: its mean of dy w h is infinite, and dx has the sign that the formula gives; zeros
+    behind the row's end, which that scale would make NaN, are not of the mean."""
+    rows = 4
+    h = torch.where(torch.arange(cols, device="cuda") % 3 == 0, -1.0, 2.0).repeat(rows, 1)
+    h[:, -1] = 1.0
+    q, s = sg.quantize_fp8(h)
+    first = (cols - 1) // B * B
+    q[2, first:] = q[2, first:].float().abs().to(E4M3)
+    s[2, -1] = float("inf")
+    dy = torch.ones(rows, cols, dtype=dtype, device="cuda")
+    w, t = torch.ones(cols, device="cuda"), torch.ones(rows, device="cuda")
+    d = sg.sandwich_norm_backward(dy, dy, (q, s), w, w, t, t)
+    sign = torch.where(torch.arange(cols, device="cuda") >= first, -1.0, -h[2].sign())
+    assert torch.equal(d.dx[2].float(), sign * float("inf"))
+    assert torch.isfinite(d.dx[[0, 1, 3]].float()).all()
