@@ -251,6 +251,33 @@ __device__ __forceinline__ bool wait_parity_bounded_cluster(uint32_t bar, uint32
   }
   return true;
 }
+// wait_parity_bounded() for what other CTAs of the cluster have stored to this CTA's shared memory: it is visible after the
+// wait, which orders shared memory only (an acquire of all memory drops the L1 cache's lines as well, at every wait).
+struct SharedOfCluster {};
+__device__ __forceinline__ bool mbar_try_wait_shared_of_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "fence.acquire.sync_restrict::shared::cluster.cluster;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_parity_bounded(uint32_t bar, uint32_t parity, uint64_t budget_ns,
+                                                    int *status, SharedOfCluster) {
+  if (mbar_try_wait_shared_of_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_shared_of_cluster(bar, parity)) {
+    if (globaltimer_ns() - t0 > budget_ns) {
+      if (status) atomicExch(status, kDevTimeout);
+      return false;
+    }
+  }
+  return true;
+}
 // 16 bytes of a peer CTA's shared memory (shared::cluster address).
 __device__ __forceinline__ float4 ld_dsmem_v4(uint32_t caddr) {
   float4 v;

@@ -101,7 +101,7 @@ class ClusterSums {
                            map_to_rank(smem_u32(to), j)),
                        "r"(__float_as_uint(s)), "r"(map_to_rank(bar, j))
                        : "memory");
-        ok = __all_sync(~0u, wait_parity_bounded(bar, calls >> 1 & 1, budget_ns, status));
+        ok = __all_sync(~0u, wait_parity_bounded(bar, calls >> 1 & 1, budget_ns, status, SharedOfCluster()));
         if (!ok) return false;
       } else {
         if (j == 0) *to = s;
