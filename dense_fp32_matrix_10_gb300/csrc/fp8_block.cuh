@@ -359,8 +359,8 @@ __device__ __forceinline__ float max_of_8(float a) {
   return a;
 }
 
-// Quotients of given values, which often have few bits and then lie between two 8-bit values: x / s from -x,
-// div = divisor(s) and ninv (see quotient()).
+// Quotients of what a caller knows (given values, and h), which often have few bits and then lie between two 8-bit values:
+// x / s from -x, div = divisor(s) and ninv (see quotient()).
 __device__ __forceinline__ float2 quotients(float2 nx, float2 div, float2 ninv) {
   const float2 q = mul2(nx, ninv);
   return fma2(fma2(q, div, nx), ninv, q);
@@ -372,8 +372,9 @@ __device__ __forceinline__ uint4 quantise_exactly(const float2 (&nx)[8], float d
   for (int i = 0; i < 8; ++i) q[i] = quotients(nx[i], both(div), both(ninv));
   return to_fp8x16<E5M2>(q);
 }
-// Quotients of computed values, which are themselves off by more than the product with the rounded 1 / s (0 for an
-// infinite scale): a correction would cost two more operations for each and bring them no nearer.
+// Quotients of values that are quantised as they are computed, which are themselves off by more than the product with the
+// rounded 1 / s (0 for an infinite scale): a correction costs two more operations for each and brings them no nearer (as
+// many 8-bit values differ from those in 64 bits; the unit's gradient 4095 x 8192 95 instead of 85 us, the unit 88.5 and 86).
 __device__ __forceinline__ float inv_of(float scale) {
   const float r = rcp_approx(scale);
   const float e = fmaf(-scale, r, 1.0f);

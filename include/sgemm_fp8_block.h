@@ -10,7 +10,10 @@
  * pass in 8 bits: its 1 x 128 quantisation as sgemm_fp8_quantize() defines it.
  * The gradients here take the matrix itself or its checkpoint (q, s), which
  * stands for q * s; the formulas are then of that value.  The quantisations'
- * own gradients are taken as the identity.
+ * own gradients are taken as the identity.  The outputs y, dg and du, which are
+ * quantised as they are computed, are multiplied by 1 / s rounded: their x / s
+ * has two FP32 roundings instead of one, so that one next to the middle of two
+ * 8-bit values may become the other of them.
  *
  * None of these calls allocates device memory, all of them may be captured
  * into a CUDA graph, sums are held in FP32 and added in a fixed order, and

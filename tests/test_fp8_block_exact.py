@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from .test_fp8 import B, E4M3, E5M2, FLOATS, rng, sg, strided  # noqa: F401
-from .test_fp8_block import halves, randn
+from .test_fp8_block import halves, randn, same
 
 gpu = pytest.mark.gpu
 
@@ -56,3 +56,23 @@ def test_an_infinite_scale_at_a_rows_end_in_the_norms_gradient(sg, cols, dtype):
     sign = torch.where(torch.arange(cols, device="cuda") >= first, -1.0, -h[2].sign())
     assert torch.equal(d.dx[2].float(), sign * float("inf"))
     assert torch.isfinite(d.dx[[0, 1, 3]].float()).all()
+
+
+# ---------------------------------------------------------------- h's checkpoint
+@gpu
+@pytest.mark.parametrize("keep", [E4M3, E5M2])
+@pytest.mark.parametrize("kind", FLOATS)
+@pytest.mark.parametrize("cols", [300, 1024, 5000, 8192, 16392])
+@pytest.mark.parametrize("few", [False, True])
+def test_the_streams_checkpoint_is_its_quantisation(sg, keep, kind, cols, few):  # noqa: F811
+    """Bit for bit what the quantiser makes of h, wherever h is known: of an FP32 output, and of a 16-bit one where a is 0 and
+    the residual is doubled (h then has the residual's bits, and many of its quotients lie between two 8-bit values; a
+    rounded 1 / s is off by enough to leave them for the wrong one)."""
+    rows = (8 << 20) // cols
+    x = randn((rows, cols), 321, torch.bfloat16 if kind == torch.float32 else kind).to(kind)
+    a = torch.zeros_like(x) if few or kind != torch.float32 else randn((rows, cols), 322)
+    w = 1 + randn(cols, 323, scale=0.1)
+    o = sg.sandwich_norm_fp8(a, x, w, w, residual_scale=2.0, training=True, checkpoint=keep)
+    assert torch.equal(o.h, 2 * x) or not few
+    for got, want in zip(o.h8, sg.quantize_fp8(o.h, dtype=keep)):
+        assert same(got, want)
