@@ -10,6 +10,8 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <optional>
+
 #include "sgemm_fp8_block.h"
 
 namespace {
@@ -327,7 +329,7 @@ class Together {
   static int64_t room(int64_t bytes) { return (bytes + 255) / 256 * 256; }
   // Whether a call's tensors are that small (the allocator's small blocks) that all of them may live as long as the last one:
   // above that, those that the backward pass keeps do not hold on to those that the next product uses up.  (Host time of 16 x
-  // 256: norms with checkpoints 8.3 us, else 10.2, their gradient 10.0 and 12.4, the unit's 6.6 and 8.3.)
+  // 256: norms with checkpoints 8.3 us, else 10.2, their gradient 10.6 and 12.4, the unit's 6.6 and 8.3.)
   static bool small(int64_t bytes) { return bytes <= (1 << 20); }
   Together(int64_t bytes, const Matrix &like) : base(empty({bytes}, like, at::kByte)) {}
   at::Tensor take(int64_t rows, int64_t cols, int64_t ld, at::ScalarType type, bool vector = false) {
@@ -470,18 +472,21 @@ PyObject *sandwich_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const bool gates = gate.t && gate.t->dim() == 2;
     const auto gate_type = gate.t ? gate.t->scalar_type() : at::kFloat;
     const int64_t gate_rows = gates ? gate.t->sizes()[0] : 0;
-    const int64_t all = 2 * rows + 3 * vector + rows_room(gate_rows, dy, gate_type) + Together::room(static_cast<int64_t>(need));
+    // (the vectors, which an optimiser may keep, hold on to each other only)
+    Together vectors((gate.t && !gates ? 3 : 2) * vector, dy);
+    const int64_t all = 2 * rows + rows_room(gate_rows, dy, gate_type) + Together::room(static_cast<int64_t>(need));
     const bool small = Together::small(all);
-    Together with(small ? all : 3 * vector, dy);
+    std::optional<Together> with;
+    if (small) with.emplace(all, dy);
     const auto matrix = [&](int64_t n, at::ScalarType type) {
-      return small ? with.take(n, dy.cols, ld, type) : empty_rows(n, dy, type);
+      return small ? with->take(n, dy.cols, ld, type) : empty_rows(n, dy, type);
     };
     at::Tensor da = matrix(dy.rows, dy.type), dx = matrix(dy.rows, dy.type), dg;
-    at::Tensor dwp = with.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
-    at::Tensor dw = with.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
-    if (gate.t) dg = gates ? matrix(gate_rows, gate_type) : with.take(1, dy.cols, dy.cols, gate_type, true);
+    at::Tensor dwp = vectors.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
+    at::Tensor dw = vectors.take(1, dy.cols, dy.cols, w.pre->scalar_type(), true);
+    if (gate.t) dg = gates ? matrix(gate_rows, gate_type) : vectors.take(1, dy.cols, dy.cols, gate_type, true);
     const int64_t floats = static_cast<int64_t>(need / 4);
-    at::Tensor ws = small ? with.take(1, floats, floats, at::kFloat, true) : empty({floats}, dy, at::kFloat);
+    at::Tensor ws = small ? with->take(1, floats, floats, at::kFloat, true) : empty({floats}, dy, at::kFloat);
     USUAL(queue(f_sandwich_backward, dy.rows, dy.cols, static_cast<float>(rho), dy.p, dy.ld, dh.p, dh.ld, type_code(dy.type),
                 A.m.p, type_code(A.m.type), A.m.ld, A.scales(), A.s.ld, H.m.p, type_code(H.m.type), H.m.ld, H.scales(),
                 H.s.ld, w.post->data_ptr(), w.pre->data_ptr(), w.type, gate.p, gate.ld, gate.type, gate.group,

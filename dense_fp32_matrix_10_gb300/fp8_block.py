@@ -13,8 +13,9 @@ pass had, they take it or its checkpoint.
 Tensors, streams and errors are as in module fp8: 2-D CUDA tensors with unit column stride and any row stride, every
 function runs on ``stream`` or torch's current stream and returns once its work is queued, nothing here computes.  The
 matrices made here have rows that start on 16-byte (8-bit) or 32-byte boundaries: a row stride rounded up to 16.  An 8-bit
-matrix and its scales may share one allocation, and so may all that a call returns for the backward pass, the vectors that
-it returns, or everything that a call makes if that is a megabyte at most.
+matrix and its scales may share one allocation, and so may all that a call returns for the backward pass, the gradients of
+weights and of a gate for all rows, or everything else that a call makes if that is a megabyte at most: what shares one is
+freed when the last of it is.
 """
 import collections
 import ctypes

@@ -76,3 +76,20 @@ def test_the_streams_checkpoint_is_its_quantisation(sg, keep, kind, cols, few): 
     assert torch.equal(o.h, 2 * x) or not few
     for got, want in zip(o.h8, sg.quantize_fp8(o.h, dtype=keep)):
         assert same(got, want)
+
+
+# ---------------------------------------------------------------- memory
+@gpu
+@pytest.mark.parametrize("rows", [1, 16, 100])
+@pytest.mark.parametrize("gate", ["none", "one", "each"])
+def test_a_weights_gradient_holds_no_more_than_the_weights(sg, rows, gate):  # noqa: F811
+    """What an optimiser keeps of a small call does not keep da, dx and the workspace as well."""
+    cols = 500
+    a, x, dy = (randn((rows, cols), 341 + i, torch.bfloat16) for i in range(3))
+    w, t = randn(cols, 344), randn(rows, 345).abs()
+    g = {"none": None, "one": w, "each": a}[gate]
+    d = sg.sandwich_norm_backward(dy, a, x, w, w, t, t, gate=g)
+    kept = [d.dweight, d.dpost_weight] + ([d.dgate] if gate == "one" else [])
+    for v in kept:
+        assert v.untyped_storage().nbytes() <= len(kept) * 2048   # 500 floats, rounded up to the allocator's 512 bytes
+        assert all(v.untyped_storage().data_ptr() != m.untyped_storage().data_ptr() for m in (d.da, d.dx))
