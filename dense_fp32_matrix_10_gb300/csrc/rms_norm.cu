@@ -11,11 +11,43 @@
 #include <mutex>
 
 #include "dispatch.h"
+#include "fp8.cuh"
 #include "fp8.h"
-#include "row_norm.cuh"
 
 namespace sg {
 namespace {
+
+constexpr int kMaxThreads = 1024;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+  return v;
+}
+
+// Sum over the threads of a row: over the warp (blockDim.x == 32: one row per
+// warp), or over the CTA (blockDim.y == 1), in a fixed order.  `red` is used
+// by turns (`turn` flips with each call), so one barrier a call is enough.
+__device__ __forceinline__ float row_sum(float v, float (*red)[32], int &turn) {
+  v = warp_sum(v);
+  if (blockDim.x == 32) return v;
+  const int warps = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  v = warp_sum(lane < warps ? red[turn][lane] : 0.0f);
+  turn ^= 1;
+  return v;
+}
+
+// Eight weights as floats.
+template <class T>
+__device__ __forceinline__ void load_w(const void *w, bool f32, int64_t c, int n, bool vec, float (&v)[8]) {
+  if (f32)
+    unpack(load8(static_cast<const float *>(w) + c, n, vec), v);
+  else
+    unpack(load8(static_cast<const T *>(w) + c, n, vec), v);
+}
 
 // vec: bit 0 x, 1 r, 2 w, 3 h, 4 y (16-byte rows), 5 q (8-byte rows)
 template <class T, int NV, bool LONG>
@@ -272,6 +304,23 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, int
   sum = warp_sum(red[threadIdx.x][threadIdx.y]);
   const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
   if (threadIdx.x == 0 && o < cols) from_float(dw + o, sum);
+}
+
+// Threads of a row and chunks of eight a thread holds.
+struct RowShape {
+  int threads, nv, rows;   // rows per CTA (threads == 32 only)
+  bool loop;
+};
+RowShape row_shape(int64_t rows, int64_t cols, int sm_count) {
+  const int64_t chunks = (cols + 7) / 8;
+  auto up32 = [](int64_t v) { return static_cast<int>((v + 31) / 32 * 32); };
+  if (chunks <= 32) return {32, 1, 8, false};
+  if (chunks <= 128 && rows >= 4 * sm_count) return {32, chunks <= 64 ? 2 : 4, 8, false};
+  // few rows: as many threads as there are chunks, for the shortest chain
+  if (chunks <= kMaxThreads && rows <= 2 * sm_count) return {up32(chunks), 1, 1, false};
+  if (chunks <= 2 * 512) return {up32((chunks + 1) / 2), 2, 1, false};
+  if (chunks <= 4 * 512) return {up32((chunks + 3) / 4), 4, 1, false};
+  return {512, 4, 1, true};
 }
 
 template <class T>
