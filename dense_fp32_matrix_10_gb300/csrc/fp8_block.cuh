@@ -41,8 +41,8 @@ __device__ __forceinline__ void store_32(void *p, const uint4 *u) {
 template <class C>
 __device__ __forceinline__ bool inside(C c, C cols) { return c >= 16 && c + 24 <= cols; }
 // Sixteen elements off 16 bytes, from the aligned units around them: their 32-bit words moved down by up to three, then
-// their bytes.  (4000 x 4001 bf16, so and with the inputs and outputs element by element: norms with checkpoints 47 and 139
-// us, their gradient 69 and 231, the unit 32 and 43, its gradient 52 and 58; with rows of 4000 38, 49, 25 and 45.)
+// their bytes.  (4000 x 4001 bf16, so and with the inputs and outputs element by element: norms with checkpoints 48 and 139
+// us, their gradient 70 and 231, the unit 32 and 43, its gradient 54 and 58.)
 template <class T>
 __device__ __forceinline__ Raw16<T> load16_across(const T *p) {
   constexpr int W = 4 * static_cast<int>(sizeof(T));   // words

@@ -239,8 +239,6 @@ __device__ __forceinline__ void finish(const SandwichGradParams &p, int64_t row,
   store16(static_cast<T *>(p.dx) + row * p.lddx + c, dx, n, level(vec, 6));
 }
 
-// KIND: a and h are 0 matrices of T, 1 checkpoints in E4M3, 2 in E5M2, 3 any of these, each its own.
-// vec: 0 dy, 1 dh, 2 w, 3 wp, 4 gate, 5 da, 6 dx, 7 a, 8 h, 9 dgate
 // Sixteen floats of this thread's own in shared memory.
 __device__ __forceinline__ void load_own(const float4 *at, float2 (&v)[8]) {
 #pragma unroll
@@ -255,6 +253,8 @@ __device__ __forceinline__ void store_own(float4 *at, const float2 (&v)[8]) {
   for (int k = 0; k < 4; ++k) at[k * kUnitStep] = make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
 }
 
+// KIND: a and h are 0 matrices of T, 1 checkpoints in E4M3, 2 in E5M2, 3 any of these, each its own.
+// vec: 0 dy, 1 dh, 2 w, 3 wp, 4 gate, 5 da, 6 dx, 7 a, 8 h, 9 dgate
 template <class T, int KIND>
 struct RowPlaces {   // 16-byte units of a thread: w, gate wp, and the next row's inputs
   static constexpr int U = sizeof(T), K = KIND == 1 || KIND == 2 ? 1 : U;

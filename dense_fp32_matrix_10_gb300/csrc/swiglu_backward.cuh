@@ -10,7 +10,7 @@
 // leaves room for one CTA of 512 threads an SM: it walks over tiles, and a
 // thread copies its elements of the next tile to places of its own in shared
 // memory while it quantises this one.  4095 x 8192 bf16 from checkpoints 85 us,
-// 3.6 TB/s, 44 instructions an element at 47 % of the issue slots (16 warps).
+// 3.6 TB/s, 45 instructions an element at 48 % of the issue slots (16 warps).
 #pragma once
 
 #include <mutex>

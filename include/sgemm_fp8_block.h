@@ -69,8 +69,8 @@ SGEMM_API sgemm_status_t sgemm_sandwich_norm_fp8(
  * otherwise; the two are independent.  DWP, DW (cols elements of typeW) and
  * DGATE (as GATE) are computed where not NULL.  workspace:
  * sgemm_sandwich_norm_backward_workspace(rows, cols) bytes, 16-byte aligned; it
- * may be NULL when DWP, DW and DGATE are.  Rows of sums have as many floats as
- * there are rows to add, in a fixed order: results repeat bit for bit.
+ * may be NULL when DWP, DW and DGATE are.  Sums over rows are added in a fixed
+ * order: results repeat bit for bit.
  * With rows == 0 DWP and DW are zeros.
  */
 SGEMM_API sgemm_status_t sgemm_sandwich_norm_backward(

@@ -8,6 +8,9 @@ Tolerances, with u = 2^-24 (FP32 rounding), derived where they are used:
   norms     t is within 2^-17 relative for given h; what h is off by comes on top, and is carried through to y.
   gradient  the formula's sums, each off by 2^-17 of its magnitudes, carried through likewise.
   unit      __expf is off by 2 + 1.173 |g| units in the last place and __fdividef by 2 (CUDA's documented bounds).
+            What the kernels do lies within these: ex2.approx is off by 2^-22 and its argument g log2(e), rounded twice, by
+            |g| 1.32 u of the result, together at most 4 u + 1.32 |g| u, and a unit in the last place is u at least, 2 u at
+            most; rcp.approx is off by one unit.
   q, s      a value that is off by E and its block's by at most E* has a scale off by E* / F and a q within half a step
             of the 8-bit type plus E / s.
 These hold for the 32-bit value; rounding to the output type is monotone, so the output lies between the bounds' own
