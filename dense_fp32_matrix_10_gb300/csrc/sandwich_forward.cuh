@@ -81,11 +81,13 @@ __device__ __forceinline__ float square_sum(const float2 (&v)[8]) {
 
 // A thread holds N times 16 consecutive elements of a row (or of a segment of it): one, with 64 registers, or two, with 80,
 // which divides a thread's fixed work (sums, offsets) by more elements and lets three rows of 8192 share an SM, but leaves
-// few rows less parallel.  With these some values are spilled (bytes a thread, stored and loaded again): two chunks with
-// checkpoints 72 and 108 (bf16) or 104 and 208 (F16), one chunk at most 60 and 60, but 224 and 144 of F32 with checkpoints and
-// 400 and 128 of its longer rows; without checkpoints at most 48 and 48.  Up to 5120 columns three rows or more share an SM either way.  One against two, in us, when they were compared: 8192 x 8192
-// bf16 with checkpoints 144 and 135, without 103 and 88; 4072 x 6144 F16 62.5 and 54.8, 52.7 and 42.2; 4072 x 5120 47.6 and
-// 50.6, 39.4 and 39.1; 4072 x 4224 44.9 and 49.5, 37.3 and 38.2; 512 x 4096 5.6 and 7.8; 4096 x 8192 F32 118 and 138.
+// few rows less parallel.  Up to 5120 columns three rows or more share an SM either way.  One against two, in us, when they
+// were compared: 8192 x 8192 bf16 with checkpoints 144 and 135, without 103 and 88; 4072 x 6144 F16 62.5 and 54.8, 52.7 and
+// 42.2; 4072 x 5120 47.6 and 50.6, 39.4 and 39.1; 4072 x 4224 44.9 and 49.5, 37.3 and 38.2; 512 x 4096 5.6 and 7.8; 4096 x 8192
+// F32 118 and 138.
+// These registers do not hold everything.  Bytes that a thread spills and loads again: two chunks with checkpoints 72 and 108
+// (bf16), 104 and 208 (F16), one chunk at most 60 and 60, but 224 and 144 of F32 with checkpoints and 400 and 128 of its longer
+// rows; without checkpoints otherwise at most 48 and 48.
 // FORM: kWarps, a row a warp and eight rows a CTA; kOne, a row a CTA; kLong, rows of more than 16384 elements, in segments
 // of that many: a three times, x twice from memory (or the L2 cache).  (A row that is the same for the whole CTA is left to
 // the uniform data path, with its offsets.)  vec: 0 a, 1 x, 2 w, 3 wp, 4 gate, and see store_outputs
